@@ -379,6 +379,186 @@ IDX_API idx_status idx_gather_k(const uint8_t* kcache, int64_t num_blocks, int32
  * ------------------------------------------------------------------------ */
 IDX_API idx_status idx_copy_async(void* dst, const void* src, size_t bytes, idx_stream_t stream);
 
+/* ===========================================================================
+ * Serving operators around the indexer: the step's page bookkeeping, the
+ * rotary tables, the insert into the attention's own key-value cache, and the
+ * attention that reads it.  The pages have no counterpart for these entries;
+ * they take and give the arrays the indexer's entries use (block tables, slot
+ * maps, positions, context lengths, the selected positions).
+ *
+ * Value types of queries, keys and values: bf16, fp16, and for the cache also
+ * FP8 E4M3 (a value is its code times the fp32 scale of its kv head).
+ * ======================================================================== */
+typedef enum {
+  IDX_BF16 = 0,
+  IDX_FP16 = 1,
+  IDX_E4M3 = 2
+} idx_dtype;
+
+/* A paged key-value cache of one attention layer (a host struct, read during
+ * the call).  Element (page p, kv head h, token o of the page, dimension d) of
+ * the keys is k[p*k_block_stride + h*k_head_stride + o*k_token_stride + d], so
+ * that a page may hold its heads one after the other or its tokens one after
+ * the other; likewise v.  Strides are in elements, nonnegative, and multiples
+ * of 16 bytes; k and v are 16-byte aligned.  Token slot s = page*page_size + o.
+ *   page_size 16, 32, 64 or 128; head_dim 64, 128 or 256;
+ *   1 <= heads <= 1024; num_blocks * page_size < 2^31.
+ *   k_scale, v_scale  [heads] fp32 on the device, for IDX_E4M3 (NULL: all 1);
+ *                     NULL for the other types. */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t num_blocks;
+  int64_t k_block_stride, k_head_stride, k_token_stride;
+  int64_t v_block_stride, v_head_stride, v_token_stride;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  int32_t dtype; /* idx_dtype */
+} idx_kv_cache;
+
+/* ---------------------------------------------------------------------------
+ * idx_plan_step -- block tables, slot maps and positions of a step, built on
+ * the GPU from request lengths.
+ *   cached_lens  [B] int32: tokens of request b already in the cache.
+ *   new_lens     [B] int32: tokens the step adds to it (0: it sits the step out).
+ *   block_table  [B, max_blocks] int32, read and written: entries
+ *                [0, ceil(cached/page_size)) are the request's pages; the
+ *                entries of the pages the step opens are written, no others.
+ *   free_pages   [num_free] int32: page ids, taken from the front in the order
+ *                of the requests and, within one, of its pages, starting at
+ *                entry pool_head[0].
+ *   pool_head    [1] int32: entries of free_pages taken so far;
+ *   pool_head_out [1] int32 out: the same after this step (another word than
+ *                pool_head, which other blocks of the launch may still read).
+ *   context_lens [B] int32 out: cached + new.
+ *   query_start  [B+1] int32 out: exclusive sums of new_lens.
+ *   slot_mapping [num_tokens] int64, positions [num_tokens] int32, token_seq
+ *                [num_tokens] int32 out: for the step's tokens, request by
+ *                request, the cache slot, the position in the request, and the
+ *                request.  Entries past the step's tokens get -1, 0 and -1.
+ * Skipped and counted in errors->bad_inputs: a negative length (the request
+ * then counts as empty), a context past INT32_MAX (it then adds nothing), a
+ * context past max_blocks pages (tokens there get slot -1), a page missing
+ * from the list or outside [0, num_blocks) (block table entry -1, its tokens
+ * slot -1), a token whose existing page id is outside the cache (slot -1), and
+ * every token past num_tokens (not written).
+ *   page_size 16, 32, 64 or 128; num_free may be 0.
+ * ------------------------------------------------------------------------ */
+IDX_API idx_status idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int32_t B,
+                         int32_t* block_table, int32_t max_blocks, const int32_t* free_pages,
+                         int32_t num_free, const int32_t* pool_head, int32_t* pool_head_out,
+                         int64_t num_blocks, int32_t page_size, int32_t* context_lens,
+                         int32_t* query_start, int64_t* slot_mapping, int32_t* positions,
+                         int32_t* token_seq, int64_t num_tokens, idx_device_errors* errors,
+                         idx_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * idx_rope_table -- rotary tables, as idx_rope_quant_q and
+ * idx_qk_norm_rope_insert take them.
+ *   cos_out, sin_out [num_pos, rot_dim/2] fp32 out: row r, column i hold
+ *              mscale * cos / sin of (pos0 + r) * w_i.
+ *   w_i        base^(-2i/rot_dim), i < rot_dim/2, scaled for long contexts by
+ *     IDX_ROPE_NONE    not at all;
+ *     IDX_ROPE_LINEAR  w_i / factor (positions interpolated);
+ *     IDX_ROPE_NTK     base * factor^(rot_dim/(rot_dim-2)) in place of base;
+ *     IDX_ROPE_YARN    w_i for the columns that make at least beta_fast turns
+ *                      over orig_len positions, w_i / factor for those that
+ *                      make at most beta_slow, a linear blend over the column
+ *                      index between (Peng et al., "YaRN", section 3.2).
+ *   mscale     factor of every entry (1, or YaRN's attention factor).
+ *   rot_dim    even, 2..256 (IDX_ROPE_NTK: 4..256); 0 <= pos0,
+ *              pos0 + num_pos <= 2^31.
+ * Angles are formed in 64-bit fixed point: beside the frequencies' own fp64
+ * rounding they are off by at most 2^-33 of a turn at any position.
+ * ------------------------------------------------------------------------ */
+typedef enum {
+  IDX_ROPE_NONE = 0,
+  IDX_ROPE_LINEAR = 1,
+  IDX_ROPE_NTK = 2,
+  IDX_ROPE_YARN = 3
+} idx_rope_scaling;
+
+IDX_API idx_status idx_rope_table(int64_t pos0, int64_t num_pos, int32_t rot_dim, double base,
+                          int32_t scaling, double factor, double orig_len, double beta_fast,
+                          double beta_slow, double mscale, float* cos_out, float* sin_out,
+                          idx_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * idx_qk_norm_rope_insert -- an attention layer's new queries, keys and values
+ * made ready in one pass: RMS norm of every query and key head
+ * (x * rsqrt(mean(x^2) + eps) * weight), rotary turn of their first rot_dim
+ * dimensions, keys and values stored into the paged cache.
+ *   q [N, Hq, D], k and v [N, Hkv, D] of type `dtype` (IDX_BF16 or IDX_FP16),
+ *              D = kv->head_dim, Hkv = kv->heads; token and head strides in
+ *              elements (multiples of 8), 16-byte aligned: e.g. slices of one
+ *              projection's output.
+ *   q_weight, k_weight [D] fp32, each may be NULL: that operand is not normed.
+ *   positions  [N] int32 rows of cos_table/sin_table [num_pos, rot_dim/2] fp32.
+ *   rot_dim    0..D, even; interleaved != 0 turns pairs (2i, 2i+1), else
+ *              (i, i + rot_dim/2), then rot_dim is a multiple of 16.
+ *              With rot_dim = 0 positions and tables are not read.
+ *   slot_mapping [N] int64; -1 = no key and value to store (q is still written).
+ *   q_out      [N, Hq, D], contiguous, of q's type; may be q itself where q is
+ *              contiguous.
+ * Arithmetic in fp32, rounded once into q_out or the cache; E4M3 codes hold
+ * x / scale, rounded to nearest even, magnitudes past 448 saturate.
+ * A token whose position is outside the table is skipped whole, one whose slot
+ * is outside [0, num_blocks*page_size) stores nothing; both are counted.
+ * ------------------------------------------------------------------------ */
+IDX_API idx_status idx_qk_norm_rope_insert(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+    int64_t v_head_stride, int64_t N, int32_t Hq, int32_t dtype, const float* q_weight,
+    const float* k_weight, float eps, const int32_t* positions, const float* cos_table,
+    const float* sin_table, int64_t num_pos, int32_t rot_dim, int32_t interleaved,
+    const int64_t* slot_mapping, void* q_out, const idx_kv_cache* kv, idx_device_errors* errors,
+    idx_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * idx_paged_attention -- attention of a few new tokens per request over the
+ * paged key-value cache, split over the cache's length and joined.
+ *   q          [B*next_n, Hq, D] of type `dtype`; row b*next_n + j is token j
+ *              of request b; token and head strides in elements (multiples of
+ *              8), 16-byte aligned.  Hq is a multiple of kv->heads; query head
+ *              h reads kv head h / (Hq / kv->heads).
+ *   kv         the cache: of q's type, or IDX_E4M3.
+ *   block_table [B, max_blocks], context_lens [B] int32 as for
+ *              idx_paged_mqa_logits: L_b counts the new tokens, row (b, j) sees
+ *              positions [0, L_b - next_n + j], with window > 0 only the last
+ *              `window` of them.
+ *   topk_idx   NULL, or [B*next_n, topk] int32: row r attends to exactly the
+ *              positions listed (as idx_paged_logits_topk leaves them; a
+ *              negative entry is none; a position listed twice counts twice).
+ *              A listed position past the row's sight is skipped and counted.
+ *              Needs window = 0.
+ *   score      s = scale * q.k, with softcap > 0: softcap * tanh(s / softcap).
+ *   out        [B*next_n, Hq, D], contiguous, of q's type: softmax(s) v.
+ *   lse        [B*next_n, Hq] fp32 or NULL: ln sum exp(s).
+ *              A row that sees nothing gets zeros and -inf.
+ *   workspace  at least idx_paged_attention_workspace_bytes(...) bytes, 256-byte
+ *              aligned, no initialisation; calls that share it must not overlap.
+ * Scores, softmax statistics and sums are fp32; the weights enter the second
+ * product as two 16-bit terms.  Results do not depend on the order in which
+ * blocks run.  Over-long contexts (clamped), negative ones (0) and page ids
+ * outside the cache (their tokens are not seen) are counted in
+ * errors->bad_inputs.
+ *   1 <= next_n <= 16; 1 <= topk <= 2^20.
+ * ------------------------------------------------------------------------ */
+IDX_API size_t idx_paged_attention_workspace_bytes(int32_t B, int32_t next_n, int32_t Hq, int32_t Hkv,
+                                           int32_t head_dim);
+
+IDX_API idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               int32_t dtype, int32_t B, int32_t next_n, int32_t Hq,
+                               const idx_kv_cache* kv, const int32_t* block_table,
+                               int32_t max_blocks, const int32_t* context_lens,
+                               const int32_t* topk_idx, int32_t topk, float scale, float softcap,
+                               int32_t window, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, idx_device_errors* errors,
+                               idx_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

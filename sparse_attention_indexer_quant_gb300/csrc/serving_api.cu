@@ -1,0 +1,404 @@
+// C ABI of the serving operators (declared in include/idx.h): argument checks,
+// workspace layout and dispatch.  Nothing here allocates device memory or
+// synchronises.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "idx.h"
+#include "launch.h"
+#include "serving.h"
+
+namespace {
+
+using idx::fail;
+using idx::ok;
+
+idx_status from_cuda(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return ok();
+  return fail(IDX_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int page_shift_of(int32_t page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+  }
+  return -1;
+}
+
+bool stride_ok(int64_t stride, int elt) {
+  return stride >= 0 && stride <= (int64_t)1 << 48 && (stride * elt) % 16 == 0;
+}
+
+// q_dtype: the type the cache must have unless it is E4M3.
+idx_status check_kv(const idx_kv_cache* kv, int32_t q_dtype) {
+  if (!kv) return fail(IDX_ERR_INVALID_ARG, "null kv");
+  if (q_dtype != IDX_BF16 && q_dtype != IDX_FP16)
+    return fail(IDX_ERR_INVALID_ARG, "dtype=%d (bf16 or fp16)", q_dtype);
+  if (kv->dtype != q_dtype && kv->dtype != IDX_E4M3)
+    return fail(IDX_ERR_INVALID_ARG, "cache dtype=%d (the queries' type or E4M3)", kv->dtype);
+  if (page_shift_of(kv->page_size) < 0)
+    return fail(IDX_ERR_INVALID_ARG, "page_size=%d (16, 32, 64 or 128)", kv->page_size);
+  if (kv->head_dim != 64 && kv->head_dim != 128 && kv->head_dim != 256)
+    return fail(IDX_ERR_INVALID_ARG, "head_dim=%d (64, 128 or 256)", kv->head_dim);
+  if (kv->heads < 1 || kv->heads > 1024)
+    return fail(IDX_ERR_INVALID_ARG, "kv heads=%d outside [1, 1024]", kv->heads);
+  if (kv->num_blocks <= 0 || kv->num_blocks > (int64_t)INT32_MAX / kv->page_size)
+    return fail(IDX_ERR_INVALID_ARG, "num_blocks=%lld", (long long)kv->num_blocks);
+  const int elt = kv->dtype == IDX_E4M3 ? 1 : 2;
+  const int64_t strides[6] = {kv->k_block_stride, kv->k_head_stride, kv->k_token_stride,
+                              kv->v_block_stride, kv->v_head_stride, kv->v_token_stride};
+  for (int64_t s : strides)
+    if (!stride_ok(s, elt))
+      return fail(IDX_ERR_INVALID_ARG, "cache stride %lld (nonnegative, a multiple of 16 bytes)",
+                  (long long)s);
+  if (kv->dtype != IDX_E4M3 && (kv->k_scale || kv->v_scale))
+    return fail(IDX_ERR_INVALID_ARG, "scales belong to an E4M3 cache");
+  return IDX_OK;
+}
+
+idx_status check_kv_pointers(const idx_kv_cache* kv) {
+  if (!kv->k || !kv->v) return fail(IDX_ERR_INVALID_ARG, "null cache");
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: k and v need 16 bytes");
+  if (!aligned(kv->k_scale, 4) || !aligned(kv->v_scale, 4))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: scales need 4 bytes");
+  return IDX_OK;
+}
+
+// Workspace of the attention: descriptors of the items, then the partials.
+struct AttnWs {
+  int2* desc;
+  float* ml;
+  float* o;
+};
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// Row tiles are counted for both row layouts (whole groups of next_n tokens;
+// one token's group with a selection) and the larger is kept.
+size_t attn_ws(void* base, int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D, AttnWs* w) {
+  const int64_t group = Hq / Hkv;
+  const int rd = idx::attn_rows_per_item(D, (int)(group * next_n));
+  const int rl = idx::attn_rows_per_item(D, (int)group);
+  const int64_t dense = B * Hkv * ((group * next_n + rd - 1) / rd);
+  const int64_t listed = B * next_n * Hkv * ((group + rl - 1) / rl);
+  const size_t items = (size_t)(dense > listed ? dense : listed);
+  const size_t rows = (size_t)(rd > rl ? rd : rl);
+  const size_t o_ml = up256(items * sizeof(int2));
+  const size_t o_o = o_ml + up256(2 * idx::kAttnMaxCtas * rows * 2 * sizeof(float));
+  if (w) {
+    uint8_t* p = static_cast<uint8_t*>(base);
+    *w = AttnWs{reinterpret_cast<int2*>(p), reinterpret_cast<float*>(p + o_ml),
+                reinterpret_cast<float*>(p + o_o)};
+  }
+  return o_o + 2 * idx::kAttnMaxCtas * rows * (size_t)D * sizeof(float);
+}
+
+bool attn_shape_ok(int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D) {
+  return B >= 0 && B <= 65535 && next_n >= 1 && next_n <= 16 && Hkv >= 1 && Hkv <= 1024 &&
+         Hq >= Hkv && Hq <= 4096 && Hq % Hkv == 0 && (D == 64 || D == 128 || D == 256) &&
+         B * next_n * Hq <= (int64_t)1 << 24;
+}
+
+}  // namespace
+
+extern "C" {
+
+idx_status idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int32_t B,
+                         int32_t* block_table, int32_t max_blocks, const int32_t* free_pages,
+                         int32_t num_free, const int32_t* pool_head, int32_t* pool_head_out,
+                         int64_t num_blocks, int32_t page_size, int32_t* context_lens,
+                         int32_t* query_start, int64_t* slot_mapping, int32_t* positions,
+                         int32_t* token_seq, int64_t num_tokens, idx_device_errors* errors,
+                         idx_stream_t stream) {
+  if (B < 0 || B > 65535) return fail(IDX_ERR_INVALID_ARG, "B=%d outside [0, 65535]", B);
+  if (max_blocks <= 0 || max_blocks > (1 << 24))
+    return fail(IDX_ERR_INVALID_ARG, "max_blocks=%d", max_blocks);
+  if (num_free < 0) return fail(IDX_ERR_INVALID_ARG, "num_free=%d", num_free);
+  const int shift = page_shift_of(page_size);
+  if (shift < 0)
+    return fail(IDX_ERR_INVALID_ARG, "page_size=%d (16, 32, 64 or 128)", page_size);
+  if (num_blocks <= 0 || num_blocks > (int64_t)INT32_MAX)
+    return fail(IDX_ERR_INVALID_ARG, "num_blocks=%lld", (long long)num_blocks);
+  if (num_tokens < 0 || num_tokens > (int64_t)INT32_MAX)
+    return fail(IDX_ERR_INVALID_ARG, "num_tokens=%lld", (long long)num_tokens);
+  int sms = 0;
+  idx_status s = idx::current_device_ok(&sms);
+  if (s != IDX_OK) return s;
+  if (!pool_head || !pool_head_out || !query_start ||
+      (B > 0 && (!cached_lens || !new_lens || !block_table || !context_lens)) ||
+      (num_free > 0 && !free_pages) ||
+      (num_tokens > 0 && (!slot_mapping || !positions || !token_seq)))
+    return fail(IDX_ERR_INVALID_ARG, "null pointer argument");
+  if (pool_head == pool_head_out)
+    return fail(IDX_ERR_INVALID_ARG, "pool_head_out must be another word than pool_head");
+  if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(free_pages, 4) || !aligned(pool_head, 4) || !aligned(pool_head_out, 4) ||
+      !aligned(context_lens, 4) || !aligned(query_start, 4) || !aligned(slot_mapping, 8) ||
+      !aligned(positions, 4) || !aligned(token_seq, 4))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: slot_mapping 8 bytes, the rest 4 bytes");
+  idx::PlanArgs a{};
+  a.cached = cached_lens;
+  a.fresh = new_lens;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.head = pool_head;
+  a.head_out = pool_head_out;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.token_seq = token_seq;
+  a.num_tokens = num_tokens;
+  a.num_blocks = num_blocks;
+  a.B = B;
+  a.max_blocks = max_blocks;
+  a.num_free = num_free;
+  a.page_shift = shift;
+  a.errors = errors;
+  return from_cuda(idx::launch_plan_step(a, sms, (cudaStream_t)stream), "plan_step launch");
+}
+
+idx_status idx_rope_table(int64_t pos0, int64_t num_pos, int32_t rot_dim, double base,
+                          int32_t scaling, double factor, double orig_len, double beta_fast,
+                          double beta_slow, double mscale, float* cos_out, float* sin_out,
+                          idx_stream_t stream) {
+  const double kPi = 3.14159265358979323846;
+  if (pos0 < 0 || num_pos < 0 || pos0 > (int64_t)1 << 31 || num_pos > ((int64_t)1 << 31) - pos0)
+    return fail(IDX_ERR_INVALID_ARG, "positions [%lld, +%lld) outside [0, 2^31)", (long long)pos0,
+                (long long)num_pos);
+  if (rot_dim < 2 || rot_dim > 2 * idx::kMaxRopeCols || rot_dim % 2 != 0)
+    return fail(IDX_ERR_INVALID_ARG, "rot_dim=%d (even, 2..256)", rot_dim);
+  if (!(base > 1.0) || !isfinite(base)) return fail(IDX_ERR_INVALID_ARG, "base=%g (> 1)", base);
+  if (scaling < IDX_ROPE_NONE || scaling > IDX_ROPE_YARN)
+    return fail(IDX_ERR_INVALID_ARG, "scaling=%d", scaling);
+  if (scaling != IDX_ROPE_NONE && (!(factor > 0.0) || !isfinite(factor)))
+    return fail(IDX_ERR_INVALID_ARG, "factor=%g (> 0)", factor);
+  if (scaling == IDX_ROPE_NTK && rot_dim < 4)
+    return fail(IDX_ERR_INVALID_ARG, "rot_dim=%d (NTK scaling needs 4)", rot_dim);
+  if (scaling == IDX_ROPE_YARN &&
+      (!(orig_len > 0.0) || !isfinite(orig_len) || !(beta_slow > 0.0) || !(beta_fast >= beta_slow) ||
+       !isfinite(beta_fast)))
+    return fail(IDX_ERR_INVALID_ARG, "orig_len=%g, beta_fast=%g, beta_slow=%g", orig_len,
+                beta_fast, beta_slow);
+  if (!isfinite(mscale)) return fail(IDX_ERR_INVALID_ARG, "mscale=%g", mscale);
+  int sms = 0;
+  idx_status s = idx::current_device_ok(&sms);
+  if (s != IDX_OK) return s;
+  if (num_pos == 0) return ok();
+  if (!cos_out || !sin_out) return fail(IDX_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(cos_out, 4) || !aligned(sin_out, 4))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: outputs need 4 bytes");
+
+  idx::RopeTableArgs a{};
+  a.half = rot_dim / 2;
+  double b = base, lo = 0.0, hi = 0.0;
+  if (scaling == IDX_ROPE_NTK) b = base * pow(factor, (double)rot_dim / (rot_dim - 2));
+  if (scaling == IDX_ROPE_YARN) {
+    // column index (in dimensions) at which a frequency makes `beta` turns over orig_len
+    auto dim_of = [&](double beta) {
+      return rot_dim * log(orig_len / (beta * 2.0 * kPi)) / (2.0 * log(base));
+    };
+    lo = fmax(floor(dim_of(beta_fast)), 0.0);
+    hi = fmin(ceil(dim_of(beta_slow)), (double)(rot_dim - 1));
+  }
+  for (int i = 0; i < a.half; ++i) {
+    double w = pow(b, -2.0 * i / rot_dim);
+    if (scaling == IDX_ROPE_LINEAR) w /= factor;
+    if (scaling == IDX_ROPE_YARN) {
+      const double ramp = fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
+      w = w * (1.0 - ramp) + w / factor * ramp;
+    }
+    const double turns = w / (2.0 * kPi);
+    // below 1, times 2^64 fits 64 bits (a double just under 1 has spare low bits)
+    a.turns[i] = (unsigned long long)ldexp(turns - floor(turns), 64);
+  }
+  a.pos0 = pos0;
+  a.num_pos = num_pos;
+  a.mscale = (float)mscale;
+  a.cos_out = cos_out;
+  a.sin_out = sin_out;
+  return from_cuda(idx::launch_rope_table(a, sms, (cudaStream_t)stream), "rope_table launch");
+}
+
+idx_status idx_qk_norm_rope_insert(
+    const void* q, int64_t q_token_stride, int64_t q_head_stride, const void* k,
+    int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride,
+    int64_t v_head_stride, int64_t N, int32_t Hq, int32_t dtype, const float* q_weight,
+    const float* k_weight, float eps, const int32_t* positions, const float* cos_table,
+    const float* sin_table, int64_t num_pos, int32_t rot_dim, int32_t interleaved,
+    const int64_t* slot_mapping, void* q_out, const idx_kv_cache* kv, idx_device_errors* errors,
+    idx_stream_t stream) {
+  idx_status s = check_kv(kv, dtype);
+  if (s != IDX_OK) return s;
+  if (N < 0 || N > (int64_t)1 << 26) return fail(IDX_ERR_INVALID_ARG, "N=%lld", (long long)N);
+  if (Hq < 1 || Hq > 4096) return fail(IDX_ERR_INVALID_ARG, "Hq=%d outside [1, 4096]", Hq);
+  if (rot_dim < 0 || rot_dim > kv->head_dim || rot_dim % 2 != 0)
+    return fail(IDX_ERR_INVALID_ARG, "rot_dim=%d (even, 0..head_dim)", rot_dim);
+  if (!interleaved && rot_dim % 16 != 0)
+    return fail(IDX_ERR_INVALID_ARG, "rot_dim=%d (a multiple of 16 for halves)", rot_dim);
+  if (num_pos < 0 || num_pos > (int64_t)1 << 31)
+    return fail(IDX_ERR_INVALID_ARG, "num_pos=%lld", (long long)num_pos);
+  if (!(eps >= 0.f) || isinf(eps)) return fail(IDX_ERR_INVALID_ARG, "eps=%g", (double)eps);
+  const int64_t strides[6] = {q_token_stride, q_head_stride, k_token_stride,
+                              k_head_stride,  v_token_stride, v_head_stride};
+  for (int64_t st : strides)
+    if (!stride_ok(st, 2))
+      return fail(IDX_ERR_INVALID_ARG, "stride %lld (nonnegative, a multiple of 8)", (long long)st);
+  // groups of lanes per block; the grid is one block per that many heads
+  if (N * (Hq + 2 * (int64_t)kv->heads) > (int64_t)INT32_MAX)
+    return fail(IDX_ERR_INVALID_ARG, "N=%lld: too many heads in all", (long long)N);
+  int sms = 0;
+  s = idx::current_device_ok(&sms);
+  if (s != IDX_OK) return s;
+  if (N == 0) return ok();
+  if ((s = check_kv_pointers(kv)) != IDX_OK) return s;
+  if (!q || !k || !v || !slot_mapping || !q_out ||
+      (rot_dim > 0 && (!positions || !cos_table || !sin_table)))
+    return fail(IDX_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: q, k, v and q_out need 16 bytes");
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4) || !aligned(positions, 4) ||
+      !aligned(cos_table, 4) || !aligned(sin_table, 4) || !aligned(slot_mapping, 8))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: slot_mapping 8 bytes, the rest 4 bytes");
+  idx::KvInsertArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.k_ts = k_token_stride;
+  a.k_hs = k_head_stride;
+  a.v_ts = v_token_stride;
+  a.v_hs = v_head_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.positions = positions;
+  a.cs = cos_table;
+  a.sn = sin_table;
+  a.num_pos = num_pos;
+  a.slots = slot_mapping;
+  a.q_out = q_out;
+  a.kv = *kv;
+  a.N = N;
+  a.Hq = Hq;
+  a.rot_dim = rot_dim;
+  a.interleaved = interleaved;
+  a.page_shift = page_shift_of(kv->page_size);
+  a.errors = errors;
+  return from_cuda(idx::launch_kv_insert(dtype, a, sms, (cudaStream_t)stream),
+                   "qk_norm_rope_insert launch");
+}
+
+size_t idx_paged_attention_workspace_bytes(int32_t B, int32_t next_n, int32_t Hq, int32_t Hkv,
+                                           int32_t head_dim) {
+  if (!attn_shape_ok(B, next_n, Hq, Hkv, head_dim)) return 0;
+  return attn_ws(nullptr, B, next_n, Hq, Hkv, head_dim, nullptr);
+}
+
+idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                               int32_t dtype, int32_t B, int32_t next_n, int32_t Hq,
+                               const idx_kv_cache* kv, const int32_t* block_table,
+                               int32_t max_blocks, const int32_t* context_lens,
+                               const int32_t* topk_idx, int32_t topk, float scale, float softcap,
+                               int32_t window, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, idx_device_errors* errors,
+                               idx_stream_t stream) {
+  idx_status s = check_kv(kv, dtype);
+  if (s != IDX_OK) return s;
+  const int D = kv->head_dim;
+  if (B < 0 || B > 65535) return fail(IDX_ERR_INVALID_ARG, "B=%d outside [0, 65535]", B);
+  if (next_n < 1 || next_n > 16) return fail(IDX_ERR_INVALID_ARG, "next_n=%d outside [1, 16]", next_n);
+  if (Hq < 1 || Hq % kv->heads != 0)
+    return fail(IDX_ERR_INVALID_ARG, "Hq=%d is no multiple of the %d kv heads", Hq, kv->heads);
+  if (!attn_shape_ok(B, next_n, Hq, kv->heads, D))
+    return fail(IDX_ERR_INVALID_ARG, "B=%d, next_n=%d, Hq=%d: too many query rows", B, next_n, Hq);
+  if (!stride_ok(q_token_stride, 2) || !stride_ok(q_head_stride, 2))
+    return fail(IDX_ERR_INVALID_ARG, "q strides %lld, %lld (nonnegative, multiples of 8)",
+                (long long)q_token_stride, (long long)q_head_stride);
+  // positions, rounded up to whole units, stay below 2^31
+  if (max_blocks <= 0 || max_blocks > (INT32_MAX - 4096) / kv->page_size)
+    return fail(IDX_ERR_INVALID_ARG, "max_blocks=%d", max_blocks);
+  if (!isfinite(scale)) return fail(IDX_ERR_INVALID_ARG, "scale=%g", (double)scale);
+  if (!(softcap >= 0.f) || isinf(softcap))
+    return fail(IDX_ERR_INVALID_ARG, "softcap=%g (>= 0)", (double)softcap);
+  if (window < 0) return fail(IDX_ERR_INVALID_ARG, "window=%d", window);
+  if (topk_idx) {
+    if (topk < 1 || topk > (1 << 20))
+      return fail(IDX_ERR_INVALID_ARG, "topk=%d outside [1, 2^20]", topk);
+    if (window != 0) return fail(IDX_ERR_INVALID_ARG, "a selection takes no window");
+  }
+  int sms = 0;
+  s = idx::current_device_ok(&sms);
+  if (s != IDX_OK) return s;
+  if (B == 0) return ok();
+  if ((s = check_kv_pointers(kv)) != IDX_OK) return s;
+  if (!q || !block_table || !context_lens || !out)
+    return fail(IDX_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: q and out need 16 bytes, workspace 256");
+  if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(topk_idx, 4) ||
+      !aligned(lse, 4))
+    return fail(IDX_ERR_INVALID_ARG, "alignment: integer arrays and lse need 4 bytes");
+  AttnWs w;
+  const size_t need = attn_ws(workspace, B, next_n, Hq, kv->heads, D, &w);
+  if (!workspace || workspace_bytes < need)
+    return fail(IDX_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, need %zu",
+                workspace ? workspace_bytes : (size_t)0, need);
+
+  idx::AttnArgs a{};
+  a.q = q;
+  a.q_ts = q_token_stride;
+  a.q_hs = q_head_stride;
+  a.kv = *kv;
+  a.block_table = block_table;
+  a.context_lens = context_lens;
+  a.topk_idx = topk_idx;
+  a.out = out;
+  a.lse = lse;
+  a.desc = w.desc;
+  a.part_ml = w.ml;
+  a.part_o = w.o;
+  a.scale = scale;
+  a.softcap = softcap;
+  // a window no context can pass is none
+  a.window = window >= max_blocks * kv->page_size ? 0 : window;
+  a.topk = topk_idx ? topk : 0;
+  a.B = B;
+  a.next_n = next_n;
+  a.Hq = Hq;
+  a.group = Hq / kv->heads;
+  a.rows = topk_idx ? a.group : a.group * next_n;
+  const int rpi = idx::attn_rows_per_item(D, a.rows);
+  a.row_tiles = (a.rows + rpi - 1) / rpi;
+  a.max_blocks = max_blocks;
+  a.page_shift = page_shift_of(kv->page_size);
+  a.q_bf16 = dtype == IDX_BF16;
+  a.errors = errors;
+
+  // Units an item can have at most, and the CTAs the device holds at once.
+  const int unit = idx::attn_unit_keys(D, kv->dtype);
+  int64_t keys = topk_idx ? topk : (int64_t)max_blocks * kv->page_size;
+  if (!topk_idx && a.window > 0 && keys > (int64_t)a.window + next_n + unit)
+    keys = (int64_t)a.window + next_n + unit;  // sight of all rows, first unit cut
+  const int64_t units = (keys + unit - 1) / unit;
+  const int64_t items = (int64_t)(topk_idx ? B * next_n : B) * kv->heads * a.row_tiles;
+  int64_t ctas = (int64_t)sms * idx::attn_ctas_per_sm(D, a.rows);
+  if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
+  a.split = units > 2;
+  const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
+  if (grid > INT32_MAX) return fail(IDX_ERR_INVALID_ARG, "too many query rows");
+  a.grid = (int32_t)grid;
+  cudaError_t e = kv->dtype == IDX_BF16   ? idx::launch_attn_bf16(a, (cudaStream_t)stream)
+                  : kv->dtype == IDX_FP16 ? idx::launch_attn_fp16(a, (cudaStream_t)stream)
+                                          : idx::launch_attn_e4m3(a, (cudaStream_t)stream);
+  if (e == cudaSuccess && a.split) e = idx::launch_attn_join(a, rpi, (cudaStream_t)stream);
+  return from_cuda(e, "paged_attention launch");
+}
+
+}  // extern "C"
