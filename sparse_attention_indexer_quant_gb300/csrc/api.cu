@@ -35,13 +35,6 @@ idx_status ok() {
   return IDX_OK;
 }
 
-}  // namespace idx
-
-namespace {
-
-using idx::fail;
-using idx::ok;
-
 // Generations of the fused call's work-item counter: distinct per call (of the
 // process), nonzero (a zero-filled workspace matches no call), below 2^40.
 unsigned long long next_item_generation() {
@@ -51,6 +44,14 @@ unsigned long long next_item_generation() {
   while (g == 0) g = g_next.fetch_add(1) & kMask;
   return g;
 }
+
+}  // namespace idx
+
+namespace {
+
+using idx::fail;
+using idx::next_item_generation;
+using idx::ok;
 
 idx_status from_cuda(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return ok();

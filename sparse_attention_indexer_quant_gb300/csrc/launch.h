@@ -13,6 +13,8 @@ namespace idx {
 // returns s; ok() clears it and returns IDX_OK.
 idx_status fail(idx_status s, const char* fmt, ...);
 idx_status ok();
+// A generation for a call's generation-tagged counters (see claim_item).
+unsigned long long next_item_generation();
 // The fail-closed device gate of every entry point, applied to the current
 // device (cached per device); *sms_out gets its SM count.
 idx_status current_device_ok(int* sms_out);

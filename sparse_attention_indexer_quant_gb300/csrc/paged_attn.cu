@@ -1,5 +1,5 @@
-// Paged attention: the join of split items, and the sizes the launch goes by
-// (the streaming kernel is in paged_attn.cuh).
+// Paged attention: the join of split items (the streaming kernel is in
+// paged_attn.cuh).
 #include "paged_attn.cuh"
 
 namespace idx {
@@ -12,24 +12,25 @@ constexpr int kJoinThreads = 128;
 // parts' sums weighted by 2^(m_part - m) in part order within each of the
 // block's lane groups, and the groups in order.  A split item has a handful of
 // parts (up to one per CTA for a lone long request); they were written a
-// moment ago and come from L2.
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a,
-                                                                 int rows_per_item) {
+// moment ago and come from L2.  The segment counter is left at this call's
+// generation with no claims, for a replay of the call.
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ float s_max[kJoinThreads / 32];
   __shared__ float4 s_acc[kJoinThreads];
   __shared__ float s_l[kJoinThreads];
   const int tid = threadIdx.x, D = a.kv.head_dim;
   const int HR = a.kv.heads * a.row_tiles;
   const int item = blockIdx.x, req = item / HR, hr = item % HR;
-  const int h = hr / a.row_tiles, rr = (hr % a.row_tiles) * rows_per_item + blockIdx.y;
+  const int h = hr / a.row_tiles, rr = (hr % a.row_tiles) * a.part_rows + blockIdx.y;
   pdl_launch_dependents();
   pdl_wait();
+  if (item == 0 && blockIdx.y == 0 && tid == 0) *a.counter = a.gen << kItemBits;
   const int2 desc = a.desc[item];
   if (desc.y <= 1 || rr >= a.rows) return;
   // part i of the item: its first CTA's, then the first part of each following CTA
   auto part_row = [&](int i) -> int64_t {
     const int part = i == 0 ? desc.x : 2 * (desc.x / 2 + i);
-    return (int64_t)part * rows_per_item + blockIdx.y;
+    return (int64_t)part * a.part_rows + blockIdx.y;
   };
   float mx = -INFINITY;
   for (int i = tid; i < desc.y; i += kJoinThreads) mx = fmaxf(mx, a.part_ml[part_row(i) * 2]);
@@ -87,20 +88,10 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
 
 }  // namespace
 
-int attn_unit_keys(int head_dim, int cache_dtype) {
-  const int row = head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2);
-  return attn::kWarps * (row >= 256 ? 16 : 32);
-}
-int attn_rows_per_item(int head_dim, int rows) { return rows > 16 && head_dim <= 128 ? 32 : 16; }
-int attn_ctas_per_sm(int head_dim, int rows) {
-  return attn_rows_per_item(head_dim, rows) == 16 && head_dim <= 128 ? 2 : 1;
-}
-
-cudaError_t launch_attn_join(const AttnArgs& a, int rows_per_item, cudaStream_t stream) {
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream) {
   const int items = (a.topk_idx ? a.B * a.next_n : a.B) * a.kv.heads * a.row_tiles;
-  const int rows = a.rows < rows_per_item ? a.rows : rows_per_item;
-  return launch_dependent(attn_join_kernel, dim3(items, rows), dim3(kJoinThreads), 0, stream, a,
-                          rows_per_item);
+  return launch_dependent(attn_join_kernel, dim3(items, a.part_rows), dim3(kJoinThreads), 0, stream,
+                          a);
 }
 
 }  // namespace idx

@@ -2,19 +2,26 @@
 //
 // Work.  An item is one kv head of one request with its query rows (next_n
 // tokens times the heads of the group; with a selection, one token's group),
-// up to 16 * MT of them.  Its keys are cut into units of 8 * KS, numbered item
-// by item over the whole batch, and CTA c of A takes units [c U / A, (c+1) U / A):
-// every CTA streams the same number of bytes whatever the requests' lengths.
-// A CTA that covers an item alone writes the result; an item that spans CTAs
-// leaves one partial (running maximum, weight, weighted sum) per CTA in the
-// workspace and a second, dependent launch joins them in the order of their
-// keys, so the result does not depend on the order in which CTAs run.
+// up to 8 * NT of them.  Its keys are cut into units of 8 * KS, numbered item
+// by item over the whole batch, and the units into segments.  With R resident
+// CTAs the first R segments take three quarters of the units, one segment per
+// CTA; the rest are cut into levels of R segments of 1/8, 1/16, ... that the
+// CTAs claim from a counter as they finish.  (Equal shares alone left the
+// fastest CTA idle for a quarter of the time: CTAs stream at rates up to 30 %
+// apart.)  Which units form a segment depends on the lengths alone, so
+// results do not depend on the order in which CTAs run.  A segment that holds
+// an item whole writes its result; an item that spans segments leaves one
+// partial (running maximum, weight, weighted sum) per segment in the workspace
+// and a second, dependent launch joins them in the order of their keys.
 //
 // Arithmetic.  o = sum_s p_s v_s / sum_s p_s with p_s = 2^(x_s - m), one pass
 // with a running reference m per row that is raised (and the sums rescaled)
 // only when a score passes it by more than 2^8, which fp32 sums hold easily:
-// most tiles need one vote instead of two shuffle reductions.  Scores and sums
-// are fp32 accumulators of m16n8k16 products with the query rows on M.  p goes
+// most tiles need one vote instead of shuffle reductions.  Scores and sums are
+// fp32 accumulators of m16n8k16 products with the keys (then the value
+// dimensions) on M and the query rows on N, so that eight rows fill a tile:
+// S^T = K Q^T, then O^T = V^T P^T, P passing from one product's result layout
+// to the other's operand layout by a register transpose (movmatrix).  p goes
 // into the second product as two 16-bit terms, hi = round(p) and lo =
 // round(p - hi): one term's rounding (2^-9 in bf16) would be as large as the
 // rounding of the output itself.  8-bit codes are exact in fp16; queries are
@@ -30,8 +37,11 @@
 // context (NaN included) cannot reach a sum.
 #pragma once
 
+#include <float.h>
+
 #include "common.cuh"
 #include "launch.h"
+#include "paged_core.cuh"
 #include "serving.h"
 #include "value_types.cuh"
 
@@ -40,33 +50,34 @@ namespace attn {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTab = 2048;  // page groups (or listed positions) resolved at a time
+constexpr int kTab = 2048;  // words of the table of resolved page groups / listed positions
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;  // log2 of how far a score may pass the reference
 
 template <int D, int CT>
 constexpr int row_bytes() { return D * (CT == IDX_E4M3 ? 1 : 2); }
-// keys per warp and unit: 4 KB half stages where rows are short
-template <int D, int CT>
-constexpr int tile_keys() { return row_bytes<D, CT>() >= 256 ? 16 : 32; }
 
-template <int D, int CT, int MT>
+template <int D, int CT, int NT>
 struct Cfg {
   static constexpr bool kF8 = CT == IDX_E4M3;
   static constexpr bool kMmaBf16 = CT == IDX_BF16;
   static constexpr int kRowB = row_bytes<D, CT>();
-  static constexpr int kKS = tile_keys<D, CT>();
+  // keys per warp and unit: 4 KB half stages where rows are short and the sums
+  // leave room for 32 keys' scores
+  static constexpr int kKS = attn_keys_per_tile(D, CT, NT);
   static constexpr int kUnit = kWarps * kKS;
-  static constexpr int kRows = 16 * MT;
+  static constexpr int kRows = 8 * NT;
   static constexpr int kHalf = kRowB * kKS;  // bytes of a half stage
   // two CTAs per SM where 128 registers a thread hold the accumulators
-  static constexpr int kOcc = (MT == 1 && D <= 128) ? 2 : 1;
+  static constexpr int kOcc = attn_occupancy(D, CT, NT);
   static constexpr int kStages = (kOcc == 2 ? 12288 : 24576) / kHalf;
   static constexpr int kRing = kStages * kHalf;
-  static constexpr int kPitch = D + 8;  // floats of a row of the merge buffer
+  static constexpr int kPitch = D + 4;  // floats of a row of the merge buffer
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSmem = kWarps * kRing + kQBytes + kTab * 4;
+  static constexpr bool kQRegs = NT == 1 && D <= 128;  // query operands stay in registers
   static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums fit its ring");
   static_assert(kStages >= 3, "");
 };
@@ -94,6 +105,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+// An 8 x 8 matrix of 16-bit values held two to a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -126,7 +143,6 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * ROWB + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Sum over a warp's lanes below / over the block, for 64-bit values.
 __device__ __forceinline__ long long warp_incl_sum(long long x, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -136,6 +152,40 @@ __device__ __forceinline__ long long warp_incl_sum(long long x, int lane) {
   return x;
 }
 
+// The cut of U units into segments by R CTAs.  One level of A = min(R, U)
+// equal segments, or K + 1 levels of R: 3/4 of the units, then 1/8, 1/16, ...,
+// 2^-(K+1), 2^-(K+1), as far as the smallest segments keep kMinSegment units.
+constexpr int kMinSegment = 3;
+struct Cut {
+  long long U;
+  int R, K;
+  __device__ Cut(long long units, int ctas) : U(units), R(ctas), K(0) {
+#pragma unroll
+    for (int k = 2; k < kAttnLevels; ++k)
+      if (U >= (long long)kMinSegment * R << (k + 1)) K = k;
+    if (K == 0 && R > U) R = (int)U;
+  }
+  __device__ int segments() const { return R * (K + 1); }
+  // weight of one segment of level l, and of all segments before level l (per CTA)
+  __device__ int weight(int l) const { return K == 0 ? 1 : (l == 0 ? 3 << (K - 1) : (l < K ? 1 << (K - 1 - l) : 1)); }
+  __device__ int before(int l) const { return l == 0 ? 0 : (2 << K) - (1 << (K - l)); }
+  __device__ long long total() const { return K == 0 ? R : (long long)R << (K + 1); }
+  // first unit of segment s (s = segments(): U)
+  __device__ long long start(int s) const {
+    const int l = s / R, i = s - l * R;
+    if (l > K) return U;
+    return ((long long)R * before(l) + (long long)i * weight(l)) * U / total();
+  }
+  // the segment that holds unit u
+  __device__ int owner(long long u) const {
+    const long long x = ((u + 1) * total() + U - 1) / U;  // least weight sum past u
+    int l = 0;
+    while (l < K && x > (long long)R * before(l + 1)) ++l;
+    const int w = weight(l);
+    return l * R + (int)((x - (long long)R * before(l) + w - 1) / w) - 1;
+  }
+};
+
 // A request as an item sees it.
 struct Span {
   int len;    // clamped context
@@ -143,16 +193,16 @@ struct Span {
   int units;  // units (at least one, so that an empty request's rows are written)
 };
 
-template <int D, int CT, int MT>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, CT, MT>::kOcc))
+template <int D, int CT, int NT>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, CT, NT>::kOcc))
 paged_attn_kernel(const __grid_constant__ AttnArgs a) {
-  using C = Cfg<D, CT, MT>;
+  using C = Cfg<D, CT, NT>;
   constexpr bool F8 = C::kF8, MB = C::kMmaBf16;
   constexpr int KS = C::kKS, ROWB = C::kRowB, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ long long s_warp[kWarps];
   __shared__ long long s_base;
-  __shared__ int s_req;
+  __shared__ int s_req, s_seg;
   __shared__ float s_mult[C::kRows];
   __shared__ float2 s_ml[kWarps][C::kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -160,7 +210,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   const uint32_t ring_u = smem_u32(ring);
   uint8_t* q_sm = smem + kWarps * C::kRing;
   const uint32_t q_u = smem_u32(q_sm);
-  int* tab = reinterpret_cast<int*>(q_sm + C::kQBytes);
+  uint32_t* tab = reinterpret_cast<uint32_t*>(q_sm + C::kQBytes);
+  // offsets into k and v: one table where both have the same strides
+  uint32_t* vtab = a.one_table ? tab : tab + kTab / 2;
+  const int tab_words = a.one_table ? kTab : kTab / 2;
 
   const bool listed = a.topk_idx != nullptr;
   const int Hkv = a.kv.heads, HR = Hkv * a.row_tiles;
@@ -178,587 +231,627 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
     return s;
   };
 
-  // ---- this CTA's units [u0, u1), and the request the first belongs to
   const int reqs = listed ? a.B * a.next_n : a.B;
   const int list_units = (a.topk + C::kUnit - 1) / C::kUnit;
-  long long u0, u1, U, A, base;  // base: first unit of request `req`
-  int req;
-  if (!a.split) {
-    U = 0;  // one CTA per item, which knows its units below
-  } else if (listed) {
-    U = (long long)reqs * HR * list_units;
-  } else {
-    long long sum = 0;
-    for (int b = tid; b < reqs; b += kThreads) sum += span_of(b).units;
-    sum = warp_incl_sum(sum, lane);
-    if (lane == 31) s_warp[warp] = sum;
-    __syncthreads();
-    U = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) U += s_warp[w];
-    U *= HR;
-  }
-  A = gridDim.x;
+  long long U = 0;
   if (a.split) {
-    // no more CTAs than units
-    if (A > U) A = U;
-    if ((long long)blockIdx.x >= A) {
-      pdl_launch_dependents();
-      return;
-    }
-    u0 = (long long)blockIdx.x * U / A;
-    u1 = ((long long)blockIdx.x + 1) * U / A;
-  } else {
-    const int units = listed ? list_units : span_of(blockIdx.x / HR).units;
-    u0 = (long long)(blockIdx.x % HR) * units;
-    u1 = u0 + units;
-  }
-  if (!a.split) {
-    req = blockIdx.x / HR;
-    base = 0;
-  } else if (listed) {
-    req = (int)(u0 / ((long long)HR * list_units));
-    base = (long long)req * HR * list_units;
-  } else {
-    long long before = 0;  // units of the requests before this round's
-    for (int b0 = 0;; b0 += kThreads) {
-      const int b = b0 + tid;
-      const long long mine = b < reqs ? (long long)span_of(b).units * HR : 0;
-      long long incl = warp_incl_sum(mine, lane);
+    if (listed) {
+      U = (long long)reqs * HR * list_units;
+    } else {
+      long long sum = 0;
+      for (int b = tid; b < reqs; b += kThreads) sum += span_of(b).units;
+      sum = warp_incl_sum(sum, lane);
+      if (lane == 31) s_warp[warp] = sum;
       __syncthreads();
-      if (lane == 31) s_warp[warp] = incl;
-      __syncthreads();
-      long long total = 0;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) incl += s_warp[w];
-        total += s_warp[w];
-      }
-      const long long start = before + incl - mine;
-      if (mine > 0 && start <= u0 && u0 < start + mine) {
-        s_req = b;
-        s_base = start;
-      }
-      before += total;
-      if (before > u0) break;
+      for (int w = 0; w < kWarps; ++w) U += s_warp[w];
+      U *= HR;
     }
-    __syncthreads();
-    req = s_req;
-    base = s_base;
   }
-
+  const Cut cut(a.split ? U : (long long)gridDim.x, (int)gridDim.x);
   const int g = lane >> 2, c4 = lane & 3;  // fragment row and column group
   const bool use_cap = a.softcap > 0.f;
 
-  for (long long u = u0; u < u1;) {
-    // ---- the item at unit u, and the part of it that is this CTA's
-    const int b = listed ? req / a.next_n : req;
-    const int tok0 = listed ? req : req * a.next_n;  // query row of the item's first row
-    const int n_tok = listed ? 1 : a.next_n;
-    const Span sp = span_of(b);
-    const int units = listed ? list_units : sp.units;
-    const int hr = (int)((u - base) / units);
-    const int h = hr / a.row_tiles, rt = hr % a.row_tiles;
-    const int ta = (int)((u - base) - (long long)hr * units);
-    const int tb = (int)min((long long)units, ta + (u1 - u));
-    const int row0 = rt * C::kRows;
-    const int rows = min(C::kRows, a.rows - row0);
-    const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + h * a.kv.k_head_stride * (F8 ? 1 : 2);
-    const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + h * a.kv.v_head_stride * (F8 ? 1 : 2);
-    const int64_t k_bs = a.kv.k_block_stride * (F8 ? 1 : 2), v_bs = a.kv.v_block_stride * (F8 ? 1 : 2);
-    const int64_t k_ts = a.kv.k_token_stride * (F8 ? 1 : 2), v_ts = a.kv.v_token_stride * (F8 ? 1 : 2);
-    // sight of query token j: [end_j - window, end_j), end_j = end0 + j
-    const int end0 = listed ? 0 : sp.len - a.next_n + 1;
-    const int lo_all = a.window > 0 ? max(0, end0 - a.window) : 0;
-    const int* bt = a.block_table + (int64_t)b * a.max_blocks;
-
-    if (tid == 0 && hr == 0 && ta == 0 && (!listed || req % a.next_n == 0)) {
-      const int L = __ldg(a.context_lens + b);
-      if (L < 0 || L > cap) count_bad_input(a.errors);
-    }
-
-    float o[MT][D / 8][4];
-    float m[MT][2], l[MT][2];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
-    }
-
-    // keys per sub-range whose page ids (or list entries) fit the table
-    constexpr int kSub = kTab / C::kUnit;            // units of listed positions
-    const int sub = listed ? kSub : kSub * 16;       // units of 16-key groups
-    bool q_loaded = false;
-    for (int sa = ta; sa < tb; sa += sub) {
-      const int sb = min(tb, sa + sub);
-      __syncthreads();  // the table and the query rows of the previous range are done with
+  for (int seg = blockIdx.x; seg < cut.segments();) {
+    // ---- the segment's units [u0, u1), and the request its first unit belongs to
+    long long u0, u1, base;  // base: first unit of request `req`
+    int req;
+    if (!a.split) {  // one CTA per item; units are counted from its request's first
+      const int units = listed ? list_units : span_of(seg / HR).units;
+      req = seg / HR;
+      base = 0;
+      u0 = (long long)(seg % HR) * units;
+      u1 = u0 + units;
+    } else {
+      u0 = cut.start(seg);
+      u1 = cut.start(seg + 1);
       if (listed) {
-        const int* list = a.topk_idx + (int64_t)req * a.topk;
-        const int my_end = max(0, sp.len - a.next_n + 1 + req % a.next_n);
-        for (int i = tid; i < (sb - sa) * C::kUnit; i += kThreads) {
-          const int at = sa * C::kUnit + i;
-          int slot = -1;
-          const int p = at < a.topk ? __ldg(list + at) : -1;
-          if (p >= 0) {
-            bool ok = p < my_end;
-            if (ok) {
-              const int id = __ldg(bt + (p >> a.page_shift));
-              ok = id >= 0 && id < a.kv.num_blocks;
-              slot = ok ? (id << a.page_shift) + (p & page_mask) : -1;
-            }
-            if (!ok && hr == 0) count_bad_input(a.errors);
-          }
-          tab[i] = slot;
-        }
+        req = (int)(u0 / ((long long)HR * list_units));
+        base = (long long)req * HR * list_units;
       } else {
-        const int g0 = (sp.t0 + sa) * (C::kUnit / 16), ng = (sb - sa) * (C::kUnit / 16);
-        for (int i = tid; i < ng; i += kThreads) {
-          const int key = (g0 + i) * 16;
-          int id = -1;
-          if (key < sp.len && key + 16 > lo_all) {
-            id = __ldg(bt + (key >> a.page_shift));
-            if (id < 0 || id >= a.kv.num_blocks) {
-              // counted once per page, by its first group that is in sight
-              if (hr == 0 && ((key & page_mask) == 0 || key <= lo_all)) count_bad_input(a.errors);
-              id = -1;
-            }
+        long long before = 0;  // units of the requests before this round's
+        for (int b0 = 0;; b0 += kThreads) {
+          const int b = b0 + tid;
+          const long long mine = b < reqs ? (long long)span_of(b).units * HR : 0;
+          long long incl = warp_incl_sum(mine, lane);
+          __syncthreads();
+          if (lane == 31) s_warp[warp] = incl;
+          __syncthreads();
+          long long total = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) incl += s_warp[w];
+            total += s_warp[w];
           }
-          tab[i] = id;
+          const long long first = before + incl - mine;
+          if (mine > 0 && first <= u0 && u0 < first + mine) {
+            s_req = b;
+            s_base = first;
+          }
+          before += total;
+          if (before > u0) break;
+        }
+        __syncthreads();
+        req = s_req;
+        base = s_base;
+      }
+    }
+
+    for (long long u = u0; u < u1;) {
+      // ---- the item at unit u, and the part of it that is this segment's
+      const int b = listed ? req / a.next_n : req;
+      const int tok0 = listed ? req : req * a.next_n;  // query row of the item's first row
+      const int n_tok = listed ? 1 : a.next_n;
+      const Span sp = span_of(b);
+      const int units = listed ? list_units : sp.units;
+      const int hr = (int)((u - base) / units);
+      const int h = hr / a.row_tiles, rt = hr % a.row_tiles;
+      const int ta = (int)((u - base) - (long long)hr * units);
+      const int tb = (int)min((long long)units, ta + (u1 - u));
+      const int row0 = rt * C::kRows;
+      const int rows = min(C::kRows, a.rows - row0);
+      constexpr int EB = F8 ? 1 : 2;  // bytes of a cached value
+      const uint8_t* kbase = static_cast<const uint8_t*>(a.kv.k) + h * a.kv.k_head_stride * EB;
+      const uint8_t* vbase = static_cast<const uint8_t*>(a.kv.v) + h * a.kv.v_head_stride * EB;
+      const int64_t k_ts = a.kv.k_token_stride * EB, v_ts = a.kv.v_token_stride * EB;
+      // a page's or token's place in 2^off_shift bytes
+      auto k_off = [&](int64_t page, int off) -> uint32_t {
+        return (uint32_t)((page * a.kv.k_block_stride * EB + off * k_ts) >> a.off_shift);
+      };
+      auto v_off = [&](int64_t page, int off) -> uint32_t {
+        return (uint32_t)((page * a.kv.v_block_stride * EB + off * v_ts) >> a.off_shift);
+      };
+      // sight of query token j: [end_j - window, end_j), end_j = end0 + j
+      const int end0 = listed ? 0 : sp.len - a.next_n + 1;
+      const int lo_all = a.window > 0 ? max(0, end0 - a.window) : 0;
+      const int* bt = a.block_table + (int64_t)b * a.max_blocks;
+      if (tid == 0 && hr == 0 && ta == 0 && (!listed || req % a.next_n == 0)) {
+        const int L = __ldg(a.context_lens + b);
+        if (L < 0 || L > cap) count_bad_input(a.errors);
+      }
+
+      // ---- the item's query rows, on their way while the table is made
+      constexpr int LQ = D / 8;  // lanes per row, 16 bytes each
+      constexpr int QP = (C::kRows * LQ + kThreads - 1) / kThreads;
+      uint4 qraw[QP];
+#pragma unroll
+      for (int i = 0; i < QP; ++i) {
+        const int r = (i * kThreads + tid) / LQ, rr = row0 + r;
+        qraw[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                                (int64_t)(tok0 + rr / a.group) * a.q_ts +
+                                (int64_t)(h * a.group + rr % a.group) * a.q_hs;
+          qraw[i] = __ldg(reinterpret_cast<const uint4*>(src) + tid % LQ);
         }
       }
-      __syncthreads();
 
-      // ---- the warp's stream: half stage 2 t is unit sa + t's keys, 2 t + 1 its values
-      const int halves = 2 * (sb - sa);
-      int put = 0, get = 0;  // ring positions
-      auto issue = [&](int i) {
-        if (i < halves) {
-          const int t = i >> 1;
-          const bool is_v = i & 1;
-          const uint8_t* src0 = is_v ? vbase : kbase;
-          const int64_t bs = is_v ? v_bs : k_bs, ts = is_v ? v_ts : k_ts;
-          constexpr int LPR = ROWB / 16, RPI = 32 / LPR;  // lanes per row, rows per pass
-          const uint32_t dst = ring_u + put * C::kHalf;
-          const int rl = lane / LPR, cl = lane % LPR;
-          if (listed) {
+      float o[NT][D / 16][4];
+      float m[NT][2], l[NT][2];
 #pragma unroll
-            for (int j = 0; j < KS / RPI; ++j) {
-              const int r = j * RPI + rl;
-              const int slot = tab[t * C::kUnit + warp * KS + r];
-              const bool ok = slot >= 0;
-              const uint8_t* src = src0 + (ok ? (slot >> a.page_shift) * bs + (slot & page_mask) * ts : 0);
-              cp_async_16_zfill(dst + swz<ROWB>(r, cl), src + cl * 16, ok);
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+        l[nt][0] = l[nt][1] = 0.f;
+      }
+
+      // units whose page groups of 16 keys (or listed positions) fit the table
+      const int sub = tab_words / (listed ? C::kUnit : C::kUnit / 16);
+      for (int sa = ta; sa < tb; sa += sub) {
+        const int sb = min(tb, sa + sub);
+        if (sa > ta) __syncthreads();  // the previous range's table is done with
+        if (listed) {
+          const int* list = a.topk_idx + (int64_t)req * a.topk;
+          const int my_end = max(0, sp.len - a.next_n + 1 + req % a.next_n);
+          for (int i = tid; i < (sb - sa) * C::kUnit; i += kThreads) {
+            const int at = sa * C::kUnit + i;
+            const int p = at < a.topk ? __ldg(list + at) : -1;
+            int id = -1;
+            if (p >= 0) {
+              if (p < my_end) {
+                id = __ldg(bt + (p >> a.page_shift));
+                if (id >= a.kv.num_blocks) id = -1;
+              }
+              if (id < 0 && hr == 0) count_bad_input(a.errors);
             }
-          } else {
-#pragma unroll
-            for (int gr = 0; gr < KS / 16; ++gr) {
-              const int grp = t * (C::kUnit / 16) + warp * (KS / 16) + gr;
-              const int id = tab[grp];
-              const int key = (sp.t0 + sa) * C::kUnit + grp * 16;
-              const uint8_t* src =
-                  src0 + (id >= 0 ? id * bs + (key & page_mask) * ts : 0) + rl * ts + cl * 16;
-#pragma unroll
-              for (int j = 0; j < 16 / RPI; ++j) {
-                const int r = j * RPI + rl;
-                const bool ok = id >= 0 && key + r < sp.len && key + r >= lo_all;
-                cp_async_16_zfill(dst + swz<ROWB>(gr * 16 + r, cl), ok ? src + (int64_t)(j * RPI) * ts : src0, ok);
+            tab[i] = id < 0 ? kNone : k_off(id, p & page_mask);
+            if (!a.one_table) vtab[i] = id < 0 ? kNone : v_off(id, p & page_mask);
+          }
+        } else {
+          const int g0 = (sp.t0 + sa) * (C::kUnit / 16), ng = (sb - sa) * (C::kUnit / 16);
+          for (int i = tid; i < ng; i += kThreads) {
+            const int key = (g0 + i) * 16;
+            int id = -1;
+            if (key < sp.len && key + 16 > lo_all) {
+              id = __ldg(bt + (key >> a.page_shift));
+              if (id < 0 || id >= a.kv.num_blocks) {
+                // counted once per page, by its first group that is in sight
+                if (hr == 0 && ((key & page_mask) == 0 || key <= lo_all)) count_bad_input(a.errors);
+                id = -1;
               }
             }
+            tab[i] = id < 0 ? kNone : k_off(id, key & page_mask);
+            if (!a.one_table) vtab[i] = id < 0 ? kNone : v_off(id, key & page_mask);
           }
         }
-        cp_async_commit();
-        put = put + 1 == NS ? 0 : put + 1;
-      };
+        if (sa == ta) {
+          // ---- query rows to shared memory
 #pragma unroll
-      for (int i = 0; i < NS; ++i) issue(i);
-
-      if (!q_loaded) {
-        q_loaded = true;
-        // ---- query rows to shared memory, one warp per row at a time
-        for (int r = warp; r < C::kRows; r += kWarps) {
-          constexpr int VL = D / 32;  // values per lane
-          float x[VL];
-          uint32_t raw[(VL + 1) / 2];
-          const int rr = row0 + r;
-          const int j = rr / a.group, head = h * a.group + rr % a.group;
-          if (r < rows) {
-            const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(tok0 + j) * a.q_ts +
-                                  (int64_t)head * a.q_hs + lane * VL;
-            const uint32_t* s32 = reinterpret_cast<const uint32_t*>(src);
+          for (int i = 0; i < QP; ++i) {
+            const int r = (i * kThreads + tid) / LQ, part = tid % LQ;
+            float mult = fabsf(a.scale);
+            uint32_t w[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
+            if (F8) {
+              float x[8], amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < VL / 2; ++i) raw[i] = s32[i];
-          } else {
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = a.q_bf16 ? unpack2<true>(w[j]) : unpack2<false>(w[j]);
+                x[2 * j] = f.x;
+                x[2 * j + 1] = f.y;
+                amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
 #pragma unroll
-            for (int i = 0; i < VL / 2; ++i) raw[i] = 0;
-          }
-          float mult = a.scale;
-          if (F8) {
-            float amax = 0.f;
+              for (int d = LQ / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
+              // largest magnitude to [2^14, 2^15): all products with codes stay finite
+              int e = 0;
+              if (a.q_bf16 && amax > 0.f && amax < INFINITY) e = 14 - ilogbf(amax);
 #pragma unroll
-            for (int i = 0; i < VL / 2; ++i) {
-              const float2 f = a.q_bf16 ? unpack2<true>(raw[i]) : unpack2<false>(raw[i]);
-              x[2 * i] = f.x;
-              x[2 * i + 1] = f.y;
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+              for (int j = 0; j < 4; ++j)
+                w[j] = pack2<false>(ldexpf(x[2 * j], e), ldexpf(x[2 * j + 1], e));
+              mult = ldexpf(mult * (a.kv.k_scale ? __ldg(a.kv.k_scale + h) : 1.f), -e);
             }
+            if (QP * kThreads == C::kRows * LQ || r < C::kRows) {
+              if (part == 0) {
+                // a masked score (-inf) times the factor must stay one: at least FLT_MIN
+                s_mult[r] = use_cap ? mult / a.softcap : fmaxf(mult * kLog2e, FLT_MIN);
+              }
+              // a negative scale is carried by the queries, so that the factor is not negative
+              const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
-            // largest magnitude to [2^14, 2^15): all products with codes stay finite
-            int e = 0;
-            if (a.q_bf16 && amax > 0.f && amax < INFINITY) e = 14 - ilogbf(amax);
-#pragma unroll
-            for (int i = 0; i < VL / 2; ++i)
-              raw[i] = pack2<false>(ldexpf(x[2 * i], e), ldexpf(x[2 * i + 1], e));
-            mult *= a.kv.k_scale ? __ldg(a.kv.k_scale + h) : 1.f;
-            mult = ldexpf(mult, -e);
-          }
-          if (lane == 0) s_mult[r] = use_cap ? mult / a.softcap : mult * kLog2e;
-#pragma unroll
-          for (int i = 0; i < VL / 2; ++i) {
-            int d = lane * VL + 2 * i;
-            // 8-bit keys come from ldmatrix four codes a lane: dimension 4c+i of a
-            // 16-block sits at k index 2c+i (i < 2) or 8+2c+i-2
-            if (F8) d = (d & ~15) + ((d & 2) ? 8 : 0) + ((d & 15) >> 2) * 2;
-            *reinterpret_cast<uint32_t*>(q_sm + swz<D * 2>(r, d >> 3) + (d & 7) * 2) = raw[i];
+              for (int j = 0; j < 4; ++j) {
+                int d = part * 8 + 2 * j;
+                // 8-bit keys come from ldmatrix four codes a lane: dimension 4c+i of a
+                // 16-block sits at k index 2c+i (i < 2) or 8+2c+i-2
+                if (F8) d = (d & ~15) + ((d & 2) ? 8 : 0) + ((d & 15) >> 2) * 2;
+                *reinterpret_cast<uint32_t*>(q_sm + swz<D * 2>(r, d >> 3) + (d & 7) * 2) = w[j] ^ flip;
+              }
+            }
           }
         }
         __syncthreads();
-      }
-      float mult[MT][2];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mult[mt][0] = s_mult[mt * 16 + g];
-        mult[mt][1] = s_mult[mt * 16 + g + 8];
-      }
 
-      for (int t = 0; t < sb - sa; ++t) {
-        // ---- scores of KS keys
-        float s[MT][KS / 8][4];
+        // ---- the warp's stream: half stage 2 t is unit sa + t's keys, 2 t + 1 its values
+        const int halves = 2 * (sb - sa);
+        int put = 0, get = 0;  // ring positions
+        auto issue = [&](int i) {
+          if (i < halves) {
+            const int t = i >> 1;
+            const bool is_v = i & 1;
+            const uint8_t* src0 = is_v ? vbase : kbase;
+            const uint32_t* tb_ = is_v ? vtab : tab;
+            constexpr int LPR = ROWB / 16, RPI = 32 / LPR;  // lanes per row, rows per pass
+            const int rl = lane / LPR, cl = lane % LPR;
+            const uint32_t dst = ring_u + put * C::kHalf;
+            src0 += cl * 16;
+            if (listed) {
+              const uint32_t* e0 = tb_ + t * C::kUnit + warp * KS + rl;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i = 0; i < KS / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
-        cp_async_wait_group<NS - 1>();
-        __syncwarp();
-        {
-          const uint32_t kt = ring_u + get * C::kHalf;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            uint32_t qa[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-              ldsm4(q_u + swz<D * 2>(mt * 16 + (lane & 15), 2 * ks + (lane >> 4)), qa[mt]);
-            if (F8) {
-              // one matrix: 8 keys x 16 codes; a lane's four codes are its k16 operand pair
-#pragma unroll
-              for (int kg = 0; kg < KS / 32; ++kg) {
-                uint32_t kb[4];
-                ldsm4(kt + swz<ROWB>(kg * 32 + lane, ks), kb);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(kb[i] & 0xFFFF));
-                  const uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(kb[i] >> 16));
-#pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) mma16816<MB>(s[mt][kg * 4 + i], qa[mt], b0, b1);
-                }
-              }
-              if (KS == 16) {
-                // 16 keys: two matrices of this step and two of the next would fit one
-                // load; the second pair is loaded again there instead
-                uint32_t kb[4];
-                ldsm4(kt + swz<ROWB>(lane & 15, ks), kb);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint32_t b0 = e4m3x2_to_f16x2((uint16_t)(kb[i] & 0xFFFF));
-                  const uint32_t b1 = e4m3x2_to_f16x2((uint16_t)(kb[i] >> 16));
-#pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) mma16816<MB>(s[mt][i], qa[mt], b0, b1);
-                }
+              for (int j = 0; j < KS / RPI; ++j) {
+                const uint32_t e = e0[j * RPI];
+                const bool ok = e != kNone;
+                cp_async_16_zfill(dst + swz<ROWB>(j * RPI + rl, cl),
+                                  src0 + (ok ? (uint64_t)e * a.off_unit : 0), ok);
               }
             } else {
+              const int64_t ts = is_v ? v_ts : k_ts;
 #pragma unroll
-              for (int kg = 0; kg < KS / 16; ++kg) {
-                uint32_t kb[4];
-                ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                     2 * ks + ((lane >> 3) & 1)), kb);
+              for (int gr = 0; gr < KS / 16; ++gr) {
+                const int grp = t * (C::kUnit / 16) + warp * (KS / 16) + gr;
+                const uint32_t e = tb_[grp];
+                const int key = (sp.t0 + sa) * C::kUnit + grp * 16 + rl;
+                const uint8_t* src = src0 + (e != kNone ? (uint64_t)e * a.off_unit + rl * ts : 0);
+                // rows of the group that some query sees: [from, to)
+                const int from = e != kNone ? lo_all - key : 16, to = sp.len - key;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma16816<MB>(s[mt][kg * 2], qa[mt], kb[0], kb[1]);
-                  mma16816<MB>(s[mt][kg * 2 + 1], qa[mt], kb[2], kb[3]);
+                for (int j = 0; j < 16 / RPI; ++j) {
+                  const bool ok = j * RPI >= from && j * RPI < to;
+                  cp_async_16_zfill(dst + swz<ROWB>(gr * 16 + j * RPI + rl, cl), ok ? src : src0, ok);
+                  src += RPI * ts;
                 }
               }
             }
           }
-        }
-        __syncwarp();
-        get = get + 1 == NS ? 0 : get + 1;
-        issue(2 * t + NS);
+          cp_async_commit();
+          put = put + 1 == NS ? 0 : put + 1;
+        };
+#pragma unroll
+        for (int i = 0; i < NS; ++i) issue(i);
 
-        // ---- log2 scores, masked
-        const int tile0 = t * C::kUnit + warp * KS;  // within the sub-range
-        const int key0 = (sp.t0 + sa) * C::kUnit + tile0;
-        bool whole;  // every key of the tile is seen by every row
-        if (listed) {
-          bool ok = true;
-          if (lane < KS) ok = tab[tile0 + lane] >= 0;
-          whole = __all_sync(~0u, ok);
-        } else {
-          bool ok = true;
+        float mult[NT][2];
+        int end[NT][2];  // first key past the row's sight
 #pragma unroll
-          for (int gr = 0; gr < KS / 16; ++gr) ok = ok && tab[tile0 / 16 + gr] >= 0;
-          whole = ok && key0 + KS <= end0 &&
-                  (a.window == 0 || key0 >= end0 + n_tok - 1 - a.window);
-        }
-        bool raise = false;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int i = 0; i < KS / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x = s[mt][i][e] * mult[mt][e >> 1];
-              if (use_cap) x = a.softcap * kLog2e * tanhf(x);
-              s[mt][i][e] = x;
-            }
-          if (!whole) {
-            int end[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = (row0 + mt * 16 + g + 8 * e) / a.group;
-              end[e] = end0 + j;
-              lo[e] = a.window > 0 ? end[e] - a.window : 0;
-            }
-#pragma unroll
-            for (int i = 0; i < KS / 8; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int kk = i * 8 + 2 * c4 + (e & 1);
-                bool seen;
-                if (listed) {
-                  seen = tab[tile0 + kk] >= 0;
-                } else {
-                  const int key = key0 + kk;
-                  seen = key < end[e >> 1] && key >= lo[e >> 1] && tab[(tile0 + kk) / 16] >= 0;
-                }
-                if (!seen) s[mt][i][e] = -INFINITY;
-              }
+          for (int e = 0; e < 2; ++e) {
+            mult[nt][e] = s_mult[nt * 8 + 2 * c4 + e];
+            end[nt][e] = end0 + (row0 + nt * 8 + 2 * c4 + e) / a.group;
           }
-          float mx[2] = {-INFINITY, -INFINITY};
+        uint32_t qf[C::kQRegs ? D / 8 : 1];
+        if (C::kQRegs) {
 #pragma unroll
-          for (int i = 0; i < KS / 8; ++i)
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t r[4];
+            ldsm4(q_u + swz<D * 2>(lane & 7, 4 * i + (lane >> 3)), r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[mt][i][e]);
-          raise = raise || mx[0] > m[mt][0] + kSlack || mx[1] > m[mt][1] + kSlack;
-        }
-        if (__any_sync(~0u, raise)) {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float mx = m[mt][e];
-#pragma unroll
-              for (int i = 0; i < KS / 8; ++i)
-                mx = fmaxf(mx, fmaxf(s[mt][i][2 * e], s[mt][i][2 * e + 1]));
-              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
-              const float f = m[mt][e] == -INFINITY ? 0.f : ex2(m[mt][e] - mx);
-              m[mt][e] = mx;
-              l[mt][e] *= f;
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i) {
-                o[mt][i][2 * e] *= f;
-                o[mt][i][2 * e + 1] *= f;
-              }
-            }
-        }
-        uint32_t ph[MT][KS / 16][4], pl[MT][KS / 16][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const float m0 = m[mt][0] == -INFINITY ? 0.f : m[mt][0];
-          const float m1 = m[mt][1] == -INFINITY ? 0.f : m[mt][1];
-#pragma unroll
-          for (int i = 0; i < KS / 8; ++i) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p0 = ex2(s[mt][i][2 * e] - (e ? m1 : m0));
-              const float p1 = ex2(s[mt][i][2 * e + 1] - (e ? m1 : m0));
-              l[mt][e] += p0 + p1;
-              const uint32_t hi = pack2<MB>(p0, p1);
-              const float2 back = unpack2<MB>(hi);
-              ph[mt][i / 2][(i & 1) * 2 + e] = hi;
-              pl[mt][i / 2][(i & 1) * 2 + e] = pack2<MB>(p0 - back.x, p1 - back.y);
-            }
+            for (int j = 0; j < 4; ++j) qf[4 * i + j] = r[j];
           }
         }
 
-        // ---- weighted sum of the values
-        cp_async_wait_group<NS - 1>();
-        __syncwarp();
-        {
-          const uint32_t vt = ring_u + get * C::kHalf;
+        for (int t = 0; t < sb - sa; ++t) {
+          // ---- scores of KS keys
+          float s[KS / 16][NT][4];
 #pragma unroll
           for (int kg = 0; kg < KS / 16; ++kg)
-            if (F8) {
-              // a matrix of 8 keys x 16 codes transposed gives a lane the codes of two
-              // keys at dimensions 2n, 2n+1: even dimensions feed one product, odd the next
 #pragma unroll
-              for (int db = 0; db < D / 32; ++db) {
-                uint32_t vb[4];
-                ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), vb);
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const uint32_t w0 = __byte_perm(vb[2 * half], 0, 0x3120);
-                  const uint32_t w1 = __byte_perm(vb[2 * half + 1], 0, 0x3120);
-                  const uint32_t e0 = e4m3x2_to_f16x2((uint16_t)(w0 & 0xFFFF));
-                  const uint32_t e1 = e4m3x2_to_f16x2((uint16_t)(w1 & 0xFFFF));
-                  const uint32_t o0 = e4m3x2_to_f16x2((uint16_t)(w0 >> 16));
-                  const uint32_t o1 = e4m3x2_to_f16x2((uint16_t)(w1 >> 16));
+              for (int e = 0; e < 4; ++e) s[kg][nt][e] = 0.f;
+          cp_async_wait_group<NS - 1>();
+          __syncwarp();
+          {
+            const uint32_t kt = ring_u + get * C::kHalf;
 #pragma unroll
-                  for (int mt = 0; mt < MT; ++mt) {
-                    const int i = (2 * db + half) * 2;
-                    mma16816<MB>(o[mt][i], ph[mt][kg], e0, e1);
-                    mma16816<MB>(o[mt][i + 1], ph[mt][kg], o0, o1);
-                    mma16816<MB>(o[mt][i], pl[mt][kg], e0, e1);
-                    mma16816<MB>(o[mt][i + 1], pl[mt][kg], o0, o1);
+            for (int k2 = 0; k2 < D / 32; ++k2) {  // 32 dimensions at a time
+              uint32_t qb[2][NT][2];
+              if (C::kQRegs) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qb[j >> 1][0][j & 1] = qf[4 * k2 + j];
+              } else if (NT == 1) {
+                uint32_t r[4];
+                ldsm4(q_u + swz<D * 2>(lane & 7, 4 * k2 + (lane >> 3)), r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qb[j >> 1][0][j & 1] = r[j];
+              } else {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                  for (int n2 = 0; n2 < NT / 2; ++n2) {
+                    uint32_t r[4];
+                    ldsm4(q_u + swz<D * 2>(n2 * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                           4 * k2 + 2 * ks + ((lane >> 3) & 1)), r);
+                    qb[ks][2 * n2][0] = r[0];
+                    qb[ks][2 * n2][1] = r[1];
+                    qb[ks][2 * n2 + 1][0] = r[2];
+                    qb[ks][2 * n2 + 1][1] = r[3];
+                  }
+              }
+#pragma unroll
+              for (int kg = 0; kg < KS / 16; ++kg) {
+                uint32_t ka[2][4];
+                if (F8) {
+                  // one matrix: 8 keys x 16 codes; a lane's four codes are its operand
+                  // values of both halves of a k16 step
+                  uint32_t r[4];
+                  ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 2 * k2 + (lane >> 4)), r);
+#pragma unroll
+                  for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                      ka[ks][hf] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + hf] & 0xFFFF));
+                      ka[ks][2 + hf] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + hf] >> 16));
+                    }
+                } else {
+#pragma unroll
+                  for (int ks = 0; ks < 2; ++ks)
+                    ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 4 * k2 + 2 * ks + (lane >> 4)), ka[ks]);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16816<MB>(s[kg][nt], ka[ks], qb[ks][nt][0], qb[ks][nt][1]);
+              }
+            }
+          }
+          __syncwarp();
+          get = get + 1 == NS ? 0 : get + 1;
+          issue(2 * t + NS);
+
+          // ---- capped and masked (a lane holds keys g, g + 8 of a group, rows 2 c4, 2 c4 + 1)
+          const int tile0 = t * C::kUnit + warp * KS;  // within the sub-range
+          const int key0 = (sp.t0 + sa) * C::kUnit + tile0;
+          bool whole;  // every key of the tile is seen by every row
+          if (listed) {
+            bool ok = true;
+            if (lane < KS) ok = tab[tile0 + lane] != kNone;
+            whole = __all_sync(~0u, ok);
+          } else {
+            bool ok = true;
+#pragma unroll
+            for (int gr = 0; gr < KS / 16; ++gr) ok = ok && tab[tile0 / 16 + gr] != kNone;
+            whole = ok && key0 + KS <= end0 &&
+                    (a.window == 0 || key0 >= end0 + n_tok - 1 - a.window);
+          }
+          if (use_cap) {
+#pragma unroll
+            for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[kg][nt][e] = a.softcap * kLog2e * tanhf(s[kg][nt][e] * mult[nt][e & 1]);
+          }
+          if (!whole) {
+#pragma unroll
+            for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const int kk = kg * 16 + hf * 8 + g;
+                const bool there = tab[listed ? tile0 + kk : (tile0 + kk) / 16] != kNone;
+                const int key = key0 + kk;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const bool seen = there && (listed || (key < end[nt][e] &&
+                                                           (a.window == 0 || key >= end[nt][e] - a.window)));
+                    if (!seen) s[kg][nt][2 * hf + e] = -INFINITY;
+                  }
+              }
+          }
+          // log2 scores are x * f with f = 1 where the cap has been applied
+          float mx[NT][2];
+          bool raise = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+              for (int kg = 1; kg < KS / 16; ++kg) x = fmaxf(x, fmaxf(s[kg][nt][e], s[kg][nt][2 + e]));
+              mx[nt][e] = use_cap ? x : x * mult[nt][e];
+              raise = raise || mx[nt][e] > m[nt][e] + kSlack;
+            }
+          if (__any_sync(~0u, raise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(mx[nt][e], m[nt][e]);
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
+                m[nt][e] = x;
+                l[nt][e] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                  o[nt][i][e] *= f;
+                  o[nt][i][2 + e] *= f;
+                }
+              }
+          }
+          // ---- weights, as two 16-bit terms in the second product's operand layout
+          uint32_t ph[KS / 16][NT][2], pl[KS / 16][NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2], r[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              f[e] = use_cap ? 1.f : mult[nt][e];
+              r[e] = m[nt][e] == -INFINITY ? 0.f : -m[nt][e];
+            }
+#pragma unroll
+            for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                const float p0 = ex2(fmaf(s[kg][nt][2 * hf], f[0], r[0]));
+                const float p1 = ex2(fmaf(s[kg][nt][2 * hf + 1], f[1], r[1]));
+                l[nt][0] += p0;
+                l[nt][1] += p1;
+                const uint32_t hi = pack2<MB>(p0, p1);
+                const float2 back = unpack2<MB>(hi);
+                ph[kg][nt][hf] = transpose8x8(hi);
+                pl[kg][nt][hf] = transpose8x8(pack2<MB>(p0 - back.x, p1 - back.y));
+              }
+          }
+
+          // ---- weighted sum of the values
+          cp_async_wait_group<NS - 1>();
+          __syncwarp();
+          {
+            const uint32_t vt = ring_u + get * C::kHalf;
+#pragma unroll
+            for (int kg = 0; kg < KS / 16; ++kg) {
+              if (F8) {
+                // a matrix of 8 keys x 16 codes transposed gives a lane two keys' codes at
+                // dimensions 2g, 2g+1: the even one is row g of the operand, the odd g + 8
+#pragma unroll
+                for (int db = 0; db < D / 32; ++db) {
+                  uint32_t r[4];
+                  ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), r);
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t va[4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                      const uint32_t w = __byte_perm(r[2 * hf + j], 0, 0x3120);
+                      va[2 * j] = e4m3x2_to_f16x2((uint16_t)(w & 0xFFFF));
+                      va[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                      mma16816<MB>(o[nt][2 * db + hf], va, ph[kg][nt][0], ph[kg][nt][1]);
+                      mma16816<MB>(o[nt][2 * db + hf], va, pl[kg][nt][0], pl[kg][nt][1]);
+                    }
+                  }
+                }
+              } else {
+#pragma unroll
+                for (int db = 0; db < D / 16; ++db) {
+                  uint32_t va[4];
+                  ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                        2 * db + ((lane >> 3) & 1)), va);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    mma16816<MB>(o[nt][db], va, ph[kg][nt][0], ph[kg][nt][1]);
+                    mma16816<MB>(o[nt][db], va, pl[kg][nt][0], pl[kg][nt][1]);
                   }
                 }
               }
-            } else {
+            }
+          }
+          __syncwarp();
+          get = get + 1 == NS ? 0 : get + 1;
+          issue(2 * t + 1 + NS);
+        }
+        cp_async_wait_group<0>();
+        __syncwarp();
+      }
+
+      // ---- the warps' sums become one: each leaves its own in its ring
+      {
+        float* buf = reinterpret_cast<float*>(ring);
 #pragma unroll
-              for (int db = 0; db < D / 16; ++db) {
-                uint32_t vb[4];
-                ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), vb);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                  mma16816<MB>(o[mt][2 * db], ph[mt][kg], vb[0], vb[1]);
-                  mma16816<MB>(o[mt][2 * db + 1], ph[mt][kg], vb[2], vb[3]);
-                  mma16816<MB>(o[mt][2 * db], pl[mt][kg], vb[0], vb[1]);
-                  mma16816<MB>(o[mt][2 * db + 1], pl[mt][kg], vb[2], vb[3]);
+          for (int e = 0; e < 2; ++e) {
+            const int r = nt * 8 + 2 * c4 + e;
+            float s = l[nt][e];
+            s += __shfl_xor_sync(~0u, s, 4);
+            s += __shfl_xor_sync(~0u, s, 8);
+            s += __shfl_xor_sync(~0u, s, 16);
+            if (r < rows) {
+              if (g == 0) s_ml[warp][r] = make_float2(m[nt][e], s);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                if (F8) {
+                  *reinterpret_cast<float2*>(buf + r * C::kPitch + i * 16 + 2 * g) =
+                      make_float2(o[nt][i][e], o[nt][i][2 + e]);
+                } else {
+                  buf[r * C::kPitch + i * 16 + g] = o[nt][i][e];
+                  buf[r * C::kPitch + i * 16 + 8 + g] = o[nt][i][2 + e];
                 }
               }
             }
-        }
-        __syncwarp();
-        get = get + 1 == NS ? 0 : get + 1;
-        issue(2 * t + 1 + NS);
-      }
-      cp_async_wait_group<0>();
-      __syncwarp();
-    }
-
-    // ---- the warps' sums become one: each leaves its own in its ring
-    {
-      float* buf = reinterpret_cast<float*>(ring);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float s = l[mt][e];
-          s += __shfl_xor_sync(~0u, s, 1);
-          s += __shfl_xor_sync(~0u, s, 2);
-          if (c4 == 0) s_ml[warp][mt * 16 + g + 8 * e] = make_float2(m[mt][e], s);
-          float* row = buf + (mt * 16 + g + 8 * e) * C::kPitch;
-#pragma unroll
-          for (int i = 0; i < D / 8; i += 2) {
-            if (F8) {
-              *reinterpret_cast<float4*>(row + i * 8 + 4 * c4) =
-                  make_float4(o[mt][i][2 * e], o[mt][i + 1][2 * e], o[mt][i][2 * e + 1],
-                              o[mt][i + 1][2 * e + 1]);
-            } else {
-              *reinterpret_cast<float2*>(row + i * 8 + 2 * c4) =
-                  make_float2(o[mt][i][2 * e], o[mt][i][2 * e + 1]);
-              *reinterpret_cast<float2*>(row + i * 8 + 8 + 2 * c4) =
-                  make_float2(o[mt][i + 1][2 * e], o[mt][i + 1][2 * e + 1]);
-            }
           }
+      }
+      const bool last_item = u + (tb - ta) >= u1;
+      if (last_item && a.split && cut.K > 0 && tid == 0) {
+        // the next segment, claimed while the sums are joined
+        const uint32_t t = claim_item(a.counter, a.gen, a.errors);
+        s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
+      }
+      __syncthreads();
+      const bool complete = ta == 0 && tb == units;
+      // partial 2 s is a segment's first part, 2 s + 1 its last; an item's parts are its
+      // first segment's last (or only) part, then the following segments' first parts
+      const int part = 2 * seg + (u == u0 ? 0 : 1);
+      if (a.split && ta == 0 && tid == 0)
+        a.desc[(long long)req * HR + hr] = make_int2(part, cut.owner(u + units - 1) - seg + 1);
+      constexpr int QPR = D / 4;  // float4 quads per row
+      for (int i = tid; i < rows * QPR; i += kThreads) {
+        const int r = i / QPR, d = (i % QPR) * 4;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_ml[w][r].x);
+        float lsum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 ml = s_ml[w][r];
+          if (ml.x == -INFINITY && ml.y == 0.f) continue;  // the warp saw nothing of this row
+          const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
+          const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kRing + (r * C::kPitch + d) * 4);
+          lsum += ml.y * f;
+          acc.x += x.x * f;
+          acc.y += x.y * f;
+          acc.z += x.z * f;
+          acc.w += x.w * f;
         }
-      }
-    }
-    __syncthreads();
-    const bool complete = ta == 0 && tb == units;
-    // partial 2c is a CTA's first part, 2c + 1 its last; an item's parts are its
-    // first CTA's last (or only) part, then the following CTAs' first parts
-    const int part = 2 * (int)blockIdx.x + (u == u0 ? 0 : 1);
-    if (a.split && ta == 0 && tid == 0) {
-      const long long last = u + units - 1;  // the item's last unit
-      const int owner = (int)(((last + 1) * A - 1) / U);
-      a.desc[(long long)req * HR + hr] = make_int2(part, owner - (int)blockIdx.x + 1);
-    }
-    constexpr int QPR = D / 4;  // float4 quads per row
-    for (int i = tid; i < rows * QPR; i += kThreads) {
-      const int r = i / QPR, d = (i % QPR) * 4;
-      float mx = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_ml[w][r].x);
-      float lsum = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w][r];
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // the warp saw nothing of this row
-        const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
-        const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kRing + (r * C::kPitch + d) * 4);
-        lsum += ml.y * f;
-        acc.x += x.x * f;
-        acc.y += x.y * f;
-        acc.z += x.z * f;
-        acc.w += x.w * f;
-      }
-      if (complete) {
-        const int rr = row0 + r;
-        const int64_t orow = (int64_t)(tok0 + rr / a.group) * a.Hq + h * a.group + rr % a.group;
-        float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-        if (F8 && a.kv.v_scale) inv *= __ldg(a.kv.v_scale + h);
-        uint2 w;
-        if (MB || (F8 && a.q_bf16)) {
-          w.x = pack2<true>(acc.x * inv, acc.y * inv);
-          w.y = pack2<true>(acc.z * inv, acc.w * inv);
+        if (complete) {
+          const int rr = row0 + r;
+          const int64_t orow = (int64_t)(tok0 + rr / a.group) * a.Hq + h * a.group + rr % a.group;
+          float inv = lsum == 0.f ? 0.f : 1.f / lsum;
+          if (F8 && a.kv.v_scale) inv *= __ldg(a.kv.v_scale + h);
+          uint2 w;
+          if (MB || (F8 && a.q_bf16)) {
+            w.x = pack2<true>(acc.x * inv, acc.y * inv);
+            w.y = pack2<true>(acc.z * inv, acc.w * inv);
+          } else {
+            w.x = pack2<false>(acc.x * inv, acc.y * inv);
+            w.y = pack2<false>(acc.z * inv, acc.w * inv);
+          }
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + d) = w;
+          if (a.lse && d == 0) a.lse[orow] = lsum == 0.f ? -INFINITY : (mx + log2f(lsum)) * kLn2;
         } else {
-          w.x = pack2<false>(acc.x * inv, acc.y * inv);
-          w.y = pack2<false>(acc.z * inv, acc.w * inv);
+          const int64_t prow = (int64_t)part * a.part_rows + r;
+          *reinterpret_cast<float4*>(a.part_o + prow * D + d) = acc;
+          if (d == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mx, lsum);
         }
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * D + d) = w;
-        if (a.lse && d == 0) a.lse[orow] = lsum == 0.f ? -INFINITY : (mx + log2f(lsum)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(a.part_o + ((int64_t)part * C::kRows + r) * D + d) = acc;
-        if (d == 0)
-          *reinterpret_cast<float2*>(a.part_ml + ((int64_t)part * C::kRows + r) * 2) = make_float2(mx, lsum);
+      }
+      __syncthreads();  // the rings, the table and the query rows are refilled next
+
+      u += tb - ta;
+      if (u - base >= (long long)units * HR) {
+        base += (long long)units * HR;
+        ++req;
       }
     }
-    __syncthreads();  // the rings are refilled next
-
-    u += tb - ta;
-    if (u - base >= (long long)units * HR) {
-      base += (long long)units * HR;
-      ++req;
-    }
+    if (!a.split || cut.K == 0) break;
+    seg = s_seg;
   }
   pdl_launch_dependents();
 }
 
-template <int D, int CT, int MT>
+template <int D, int CT, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, CT, MT>;
+  using C = Cfg<D, CT, NT>;
   static const cudaError_t attr = cudaFuncSetAttribute(
-      paged_attn_kernel<D, CT, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+      paged_attn_kernel<D, CT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (attr != cudaSuccess) return attr;
-  return launch_dependent(paged_attn_kernel<D, CT, MT>, dim3(a.grid), dim3(kThreads), C::kSmem,
+  return launch_dependent(paged_attn_kernel<D, CT, NT>, dim3(a.grid), dim3(kThreads), C::kSmem,
                           stream, a);
+}
+
+template <int D, int CT>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
+  switch (attn_row_tiles(D, a.rows)) {
+    case 1: return launch<D, CT, 1>(a, stream);
+    case 2: return launch<D, CT, 2>(a, stream);
+  }
+  if constexpr (D <= 128) return launch<D, CT, 4>(a, stream);
+  return cudaErrorInvalidValue;
 }
 
 template <int CT>
 cudaError_t launch_type(const AttnArgs& a, cudaStream_t stream) {
-  const bool two = attn_rows_per_item(a.kv.head_dim, a.rows) == 32;
   switch (a.kv.head_dim) {
-    case 64: return two ? launch<64, CT, 2>(a, stream) : launch<64, CT, 1>(a, stream);
-    case 128: return two ? launch<128, CT, 2>(a, stream) : launch<128, CT, 1>(a, stream);
-    default: return launch<256, CT, 1>(a, stream);
+    case 64: return launch_rows<64, CT>(a, stream);
+    case 128: return launch_rows<128, CT>(a, stream);
+    default: return launch_rows<256, CT>(a, stream);
   }
 }
 

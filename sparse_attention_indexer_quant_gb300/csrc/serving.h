@@ -69,9 +69,12 @@ struct KvInsertArgs {
 };
 cudaError_t launch_kv_insert(int dtype, const KvInsertArgs& a, int sms, cudaStream_t stream);
 
-// Paged attention: resident CTAs over the device are bounded by this, so that
-// the workspace's size does not depend on the device.
+// Paged attention: resident CTAs over the device, and the levels of segments
+// they claim (see paged_attn.cuh), are bounded by these, so that the
+// workspace's size depends on neither the device nor the lengths.
 constexpr int kAttnMaxCtas = 320;
+constexpr int kAttnLevels = 5;
+constexpr int kAttnMaxParts = 2 * kAttnLevels * kAttnMaxCtas;
 struct AttnArgs {
   const void* q;
   int64_t q_ts, q_hs;  // elements
@@ -81,9 +84,11 @@ struct AttnArgs {
   const int32_t* topk_idx;  // null: the whole context
   void* out;
   float* lse;
-  float* part_o;   // [2 * kAttnMaxCtas][rows][D] partial sums of split items
-  float* part_ml;  // [2 * kAttnMaxCtas][rows][2] their running maxima and weights
+  float* part_o;   // [kAttnMaxParts][part_rows][D] partial sums of split items
+  float* part_ml;  // [kAttnMaxParts][part_rows][2] their running maxima and weights
   int2* desc;      // [items] first partial and number of partials
+  unsigned long long* counter;  // generation-tagged count of claimed segments
+  unsigned long long gen;       // this call's generation
   float scale;
   float softcap;
   int32_t window;
@@ -92,22 +97,40 @@ struct AttnArgs {
   int32_t next_n;
   int32_t Hq;
   int32_t group;    // query heads per kv head
-  int32_t rows;     // query rows of one item's kv head: next_n * group, or group (top-k)
+  int32_t rows;     // query rows of one kv head: next_n * group, or group (top-k)
   int32_t row_tiles;
+  int32_t part_rows;  // query rows of an item: at most 8 * attn_row_tiles()
   int32_t max_blocks;
   int32_t page_shift;
-  int32_t q_bf16;   // type of q and out
-  int32_t split;    // 0: one CTA per item, no join
+  int32_t off_shift;  // every page and token offset is a multiple of 2^off_shift bytes,
+  uint32_t off_unit;  // off_unit, and fits 32 bits in that unit
+  int32_t one_table;  // k and v have the same page and token strides
+  int32_t q_bf16;     // type of q and out
+  int32_t split;      // 0: one CTA per item, no join
   int32_t grid;
   idx_device_errors* errors;
 };
-// keys one CTA handles at a time (the unit in which an item's length is split)
-int attn_unit_keys(int head_dim, int cache_dtype);
-int attn_rows_per_item(int head_dim, int rows);
-int attn_ctas_per_sm(int head_dim, int rows);
+// Tiles of eight query rows an item of `rows` rows takes: 1, 2 or 4 (head_dim
+// 256: 1 or 2, where four would not fit the registers).
+constexpr int attn_row_tiles(int head_dim, int rows) {
+  return rows <= 8 ? 1 : (rows <= 16 || head_dim > 128 ? 2 : 4);
+}
+constexpr int attn_keys_per_tile(int head_dim, int cache_dtype, int nt) {
+  return head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) >= 256 || nt == 4 ? 16 : 32;
+}
+// Resident CTAs per SM: two where the sums take at most 64 registers a thread
+// and three half stages fit 12 KB of shared memory a warp.
+constexpr int attn_occupancy(int head_dim, int cache_dtype, int nt) {
+  return head_dim * nt <= 256 && 3 * head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) *
+                                         attn_keys_per_tile(head_dim, cache_dtype, nt) <= 12288 ? 2 : 1;
+}
+// keys a CTA handles at a time (the unit in which an item's length is split)
+constexpr int attn_unit_keys(int head_dim, int cache_dtype, int nt) {
+  return 8 * attn_keys_per_tile(head_dim, cache_dtype, nt);
+}
 cudaError_t launch_attn_bf16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_fp16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_e4m3(const AttnArgs& a, cudaStream_t stream);
-cudaError_t launch_attn_join(const AttnArgs& a, int rows_per_item, cudaStream_t stream);
+cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace idx

@@ -71,31 +71,42 @@ idx_status check_kv_pointers(const idx_kv_cache* kv) {
   return IDX_OK;
 }
 
-// Workspace of the attention: descriptors of the items, then the partials.
+// Workspace of the attention: the segment counter, the items' descriptors, then
+// the partials (rows of the larger of the two row layouts: whole groups of
+// next_n tokens, or one token's group with a selection).
 struct AttnWs {
+  unsigned long long* counter;
   int2* desc;
   float* ml;
   float* o;
 };
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-// Row tiles are counted for both row layouts (whole groups of next_n tokens;
-// one token's group with a selection) and the larger is kept.
+int64_t part_rows_of(int D, int64_t rows) {
+  const int64_t most = 8 * idx::attn_row_tiles(D, (int)rows);
+  return rows < most ? rows : most;
+}
 size_t attn_ws(void* base, int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D, AttnWs* w) {
   const int64_t group = Hq / Hkv;
-  const int rd = idx::attn_rows_per_item(D, (int)(group * next_n));
-  const int rl = idx::attn_rows_per_item(D, (int)group);
-  const int64_t dense = B * Hkv * ((group * next_n + rd - 1) / rd);
-  const int64_t listed = B * next_n * Hkv * ((group + rl - 1) / rl);
+  const int64_t rows = part_rows_of(D, group * next_n), one = part_rows_of(D, group);
+  const int64_t dense = B * Hkv * ((group * next_n + rows - 1) / rows);
+  const int64_t listed = B * next_n * Hkv * ((group + one - 1) / one);
   const size_t items = (size_t)(dense > listed ? dense : listed);
-  const size_t rows = (size_t)(rd > rl ? rd : rl);
-  const size_t o_ml = up256(items * sizeof(int2));
-  const size_t o_o = o_ml + up256(2 * idx::kAttnMaxCtas * rows * 2 * sizeof(float));
+  const size_t o_desc = 256;
+  const size_t o_ml = o_desc + up256(items * sizeof(int2));
+  const size_t o_o = o_ml + up256(idx::kAttnMaxParts * (size_t)rows * 2 * sizeof(float));
   if (w) {
     uint8_t* p = static_cast<uint8_t*>(base);
-    *w = AttnWs{reinterpret_cast<int2*>(p), reinterpret_cast<float*>(p + o_ml),
-                reinterpret_cast<float*>(p + o_o)};
+    *w = AttnWs{reinterpret_cast<unsigned long long*>(p), reinterpret_cast<int2*>(p + o_desc),
+                reinterpret_cast<float*>(p + o_ml), reinterpret_cast<float*>(p + o_o)};
   }
-  return o_o + 2 * idx::kAttnMaxCtas * rows * (size_t)D * sizeof(float);
+  return o_o + idx::kAttnMaxParts * (size_t)rows * (size_t)D * sizeof(float);
+}
+
+// The largest power of two (at least 16 bytes, at most 2^30) that divides both.
+int common_shift(int64_t x, int64_t y) {
+  int s = 4;
+  while (s < 30 && ((x | y) >> s & 1) == 0) ++s;
+  return s;
 }
 
 bool attn_shape_ok(int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D) {
@@ -345,6 +356,21 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   if (!aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(topk_idx, 4) ||
       !aligned(lse, 4))
     return fail(IDX_ERR_INVALID_ARG, "alignment: integer arrays and lse need 4 bytes");
+  // page and token offsets as 32-bit multiples of a power of two
+  const int elt = kv->dtype == IDX_E4M3 ? 1 : 2;
+  const bool one_table = kv->k_block_stride == kv->v_block_stride &&
+                         kv->k_token_stride == kv->v_token_stride;
+  const int shift_k = common_shift(kv->k_block_stride * elt, kv->k_token_stride * elt);
+  const int shift_v = common_shift(kv->v_block_stride * elt, kv->v_token_stride * elt);
+  const int off_shift = shift_k < shift_v ? shift_k : shift_v;
+  auto span = [&](int64_t bs, int64_t ts) {
+    return (double)(kv->num_blocks - 1) * (double)bs + (double)(kv->page_size - 1) * (double)ts;
+  };
+  const double far = fmax(span(kv->k_block_stride, kv->k_token_stride),
+                          span(kv->v_block_stride, kv->v_token_stride)) * elt;
+  if (far >= ldexp(4294967295.0, off_shift))
+    return fail(IDX_ERR_INVALID_ARG, "the cache spans %g bytes: strides must then be multiples of more than %d bytes",
+                far, 1 << off_shift);
   AttnWs w;
   const size_t need = attn_ws(workspace, B, next_n, Hq, kv->heads, D, &w);
   if (!workspace || workspace_bytes < need)
@@ -361,6 +387,8 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   a.topk_idx = topk_idx;
   a.out = out;
   a.lse = lse;
+  a.counter = w.counter;
+  a.gen = idx::next_item_generation();
   a.desc = w.desc;
   a.part_ml = w.ml;
   a.part_o = w.o;
@@ -374,21 +402,25 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   a.Hq = Hq;
   a.group = Hq / kv->heads;
   a.rows = topk_idx ? a.group : a.group * next_n;
-  const int rpi = idx::attn_rows_per_item(D, a.rows);
-  a.row_tiles = (a.rows + rpi - 1) / rpi;
+  const int nt = idx::attn_row_tiles(D, a.rows);
+  a.part_rows = (int32_t)part_rows_of(D, a.rows);
+  a.row_tiles = (a.rows + 8 * nt - 1) / (8 * nt);
   a.max_blocks = max_blocks;
   a.page_shift = page_shift_of(kv->page_size);
+  a.off_shift = off_shift;
+  a.off_unit = 1u << off_shift;
+  a.one_table = one_table;
   a.q_bf16 = dtype == IDX_BF16;
   a.errors = errors;
 
   // Units an item can have at most, and the CTAs the device holds at once.
-  const int unit = idx::attn_unit_keys(D, kv->dtype);
+  const int unit = idx::attn_unit_keys(D, kv->dtype, nt);
   int64_t keys = topk_idx ? topk : (int64_t)max_blocks * kv->page_size;
   if (!topk_idx && a.window > 0 && keys > (int64_t)a.window + next_n + unit)
     keys = (int64_t)a.window + next_n + unit;  // sight of all rows, first unit cut
   const int64_t units = (keys + unit - 1) / unit;
   const int64_t items = (int64_t)(topk_idx ? B * next_n : B) * kv->heads * a.row_tiles;
-  int64_t ctas = (int64_t)sms * idx::attn_ctas_per_sm(D, a.rows);
+  int64_t ctas = (int64_t)sms * idx::attn_occupancy(D, kv->dtype, nt);
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
   a.split = units > 2;
   const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
@@ -397,7 +429,7 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   cudaError_t e = kv->dtype == IDX_BF16   ? idx::launch_attn_bf16(a, (cudaStream_t)stream)
                   : kv->dtype == IDX_FP16 ? idx::launch_attn_fp16(a, (cudaStream_t)stream)
                                           : idx::launch_attn_e4m3(a, (cudaStream_t)stream);
-  if (e == cudaSuccess && a.split) e = idx::launch_attn_join(a, rpi, (cudaStream_t)stream);
+  if (e == cudaSuccess && a.split) e = idx::launch_attn_join(a, (cudaStream_t)stream);
   return from_cuda(e, "paged_attention launch");
 }
 
