@@ -18,10 +18,11 @@
 // with a running reference m per row that is raised (and the sums rescaled)
 // only when a score passes it by more than 2^8, which fp32 sums hold easily:
 // most tiles need one vote instead of shuffle reductions.  Scores and sums are
-// fp32 accumulators of m16n8k16 products with the keys (then the value
-// dimensions) on M and the query rows on N, so that eight rows fill a tile:
-// S^T = K Q^T, then O^T = V^T P^T, P passing from one product's result layout
-// to the other's operand layout by a register transpose (movmatrix).  p goes
+// fp32 accumulators of m16n8k16 products.  Up to eight rows: keys (then value
+// dimensions) on M, query rows on N, so that eight rows fill a tile: S^T =
+// K Q^T, then O^T = V^T P^T, P passing from one product's result layout to the
+// other's operand layout by a register transpose (movmatrix).  More rows: query
+// rows on M.  p goes
 // into the second product as two 16-bit terms, hi = round(p) and lo =
 // round(p - hi): one term's rounding (2^-9 in bf16) would be as large as the
 // rounding of the output itself.  8-bit codes are exact in fp16; queries are
@@ -77,11 +78,13 @@ struct Cfg {
   static constexpr int kPitch = D + 4;  // floats of a row of the merge buffer
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSmem = kWarps * kRing + kQBytes + kTab * 4;
-  static constexpr bool kQRegs = NT == 1 && D <= 128;  // query operands stay in registers
   static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums fit its ring");
   static_assert(kStages >= 3, "");
 };
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, bool full) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(full ? 16 : 0)
@@ -186,6 +189,455 @@ struct Cut {
   }
 };
 
+// What a tile's masking goes by: key kk of the tile (keys key0 ..) is seen by
+// row r where the table has its place and it lies in [end_r - window, end_r).
+struct Sight {
+  const uint32_t* tab;  // of the sub-range
+  const int* end;       // per row of the item, in shared memory
+  int tile0, key0, window;
+  bool listed;
+  __device__ __forceinline__ bool there(int kk) const {
+    return tab[listed ? tile0 + kk : (tile0 + kk) / 16] != kNone;
+  }
+  __device__ __forceinline__ bool in(int kk, int r) const {
+    const int key = key0 + kk, e = end[r];
+    return listed || (key < e && (window == 0 || key >= e - window));
+  }
+};
+
+// Two weights of one row pair or key pair, as the fp16/bf16 term and the rest.
+template <bool MB>
+__device__ __forceinline__ void two_terms(float p0, float p1, uint32_t* hi, uint32_t* lo) {
+  *hi = pack2<MB>(p0, p1);
+  const float2 back = unpack2<MB>(*hi);
+  *lo = pack2<MB>(p0 - back.x, p1 - back.y);
+}
+
+// One warp's running sums over its tiles, for at most eight query rows: keys
+// (then value dimensions) on M, rows on N.  A lane holds keys g, g + 8 of a
+// 16-key group and rows 2 c4, 2 c4 + 1.
+template <int D, int CT, int KS>
+struct KeysOnM {
+  static constexpr bool F8 = CT == IDX_E4M3, MB = CT == IDX_BF16;
+  static constexpr int ROWB = row_bytes<D, CT>();
+  static constexpr bool kQRegs = D <= 128;  // query operands stay in registers
+  float o[D / 16][4], s[KS / 16][4], m[2], l[2];
+  uint32_t qf[kQRegs ? D / 8 : 1];
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+  }
+  __device__ __forceinline__ void load_q(uint32_t q_u, int lane) {
+    if (!kQRegs) return;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t r[4];
+      ldsm4(q_u + swz<D * 2>(lane & 7, 4 * i + (lane >> 3)), r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qf[4 * i + j] = r[j];
+    }
+  }
+  __device__ __forceinline__ void scores(uint32_t kt, uint32_t q_u, int lane) {
+#pragma unroll
+    for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[kg][e] = 0.f;
+#pragma unroll
+    for (int k2 = 0; k2 < D / 32; ++k2) {  // 32 dimensions at a time
+      uint32_t qb[4];
+      if (kQRegs) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) qb[j] = qf[4 * k2 + j];
+      } else {
+        ldsm4(q_u + swz<D * 2>(lane & 7, 4 * k2 + (lane >> 3)), qb);
+      }
+#pragma unroll
+      for (int kg = 0; kg < KS / 16; ++kg) {
+        uint32_t ka[2][4];
+        if (F8) {
+          // one matrix: 8 keys x 16 codes; a lane's four codes are its operand
+          // values of both halves of a k16 step
+          uint32_t r[4];
+          ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 2 * k2 + (lane >> 4)), r);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              ka[ks][hf] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + hf] & 0xFFFF));
+              ka[ks][2 + hf] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + hf] >> 16));
+            }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 4 * k2 + 2 * ks + (lane >> 4)), ka[ks]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) mma16816<MB>(s[kg], ka[ks], qb[2 * ks], qb[2 * ks + 1]);
+      }
+    }
+  }
+  __device__ __forceinline__ void cap(float softcap, const float* mult, int lane) {
+    const float2 f = *reinterpret_cast<const float2*>(mult + 2 * (lane & 3));
+#pragma unroll
+    for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        s[kg][e] = softcap * kLog2e * tanhf(s[kg][e] * (e & 1 ? f.y : f.x));
+  }
+  __device__ __forceinline__ void mask(const Sight& v, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int kk = kg * 16 + hf * 8 + g;
+        const bool there = v.there(kk);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (!there || !v.in(kk, 2 * c4 + e)) s[kg][2 * hf + e] = -INFINITY;
+      }
+  }
+  // Reference raised where needed, weights, and their product with the values.
+  // Log2 scores are s * mult.
+  __device__ __forceinline__ void values(uint32_t vt, float2 mult, int lane) {
+    const float f[2] = {mult.x, mult.y};
+    float mx[2];
+    bool raise = false;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = fmaxf(s[0][e], s[0][2 + e]);
+#pragma unroll
+      for (int kg = 1; kg < KS / 16; ++kg) x = fmaxf(x, fmaxf(s[kg][e], s[kg][2 + e]));
+      mx[e] = x * f[e];
+      raise = raise || mx[e] > m[e] + kSlack;
+    }
+    if (__any_sync(~0u, raise)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(mx[e], m[e]);
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+        const float w = m[e] == -INFINITY ? 0.f : ex2(m[e] - x);
+        m[e] = x;
+        l[e] *= w;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          o[i][e] *= w;
+          o[i][2 + e] *= w;
+        }
+      }
+    }
+    const float r0 = m[0] == -INFINITY ? 0.f : -m[0], r1 = m[1] == -INFINITY ? 0.f : -m[1];
+#pragma unroll
+    for (int kg = 0; kg < KS / 16; ++kg) {
+      uint32_t ph[2], pl[2];  // the weights in the second product's operand layout
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const float p0 = ex2(fmaf(s[kg][2 * hf], f[0], r0));
+        const float p1 = ex2(fmaf(s[kg][2 * hf + 1], f[1], r1));
+        l[0] += p0;
+        l[1] += p1;
+        uint32_t hi, lo;
+        two_terms<MB>(p0, p1, &hi, &lo);
+        ph[hf] = transpose8x8(hi);
+        pl[hf] = transpose8x8(lo);
+      }
+      if (F8) {
+        // a matrix of 8 keys x 16 codes transposed gives a lane two keys' codes at
+        // dimensions 2g, 2g+1: the even one is row g of the operand, the odd g + 8
+#pragma unroll
+        for (int db = 0; db < D / 32; ++db) {
+          uint32_t r[4];
+          ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), r);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t va[4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t w = __byte_perm(r[2 * hf + j], 0, 0x3120);
+              va[2 * j] = e4m3x2_to_f16x2((uint16_t)(w & 0xFFFF));
+              va[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+            }
+            mma16816<MB>(o[2 * db + hf], va, ph[0], ph[1]);
+            mma16816<MB>(o[2 * db + hf], va, pl[0], pl[1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db) {
+          uint32_t va[4];
+          ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                2 * db + ((lane >> 3) & 1)), va);
+          mma16816<MB>(o[db], va, ph[0], ph[1]);
+          mma16816<MB>(o[db], va, pl[0], pl[1]);
+        }
+      }
+    }
+  }
+  // This lane's factors of the rows it holds.
+  __device__ __forceinline__ float2 factors(const float* mult, int lane) const {
+    return *reinterpret_cast<const float2*>(mult + 2 * (lane & 3));
+  }
+  __device__ __forceinline__ void leave(float* buf, int pitch, float2* ml, int rows, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = 2 * c4 + e;
+      float x = l[e];
+      x += __shfl_xor_sync(~0u, x, 4);
+      x += __shfl_xor_sync(~0u, x, 8);
+      x += __shfl_xor_sync(~0u, x, 16);
+      if (r < rows) {
+        if (g == 0) ml[r] = make_float2(m[e], x);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          if (F8) {
+            *reinterpret_cast<float2*>(buf + r * pitch + i * 16 + 2 * g) = make_float2(o[i][e], o[i][2 + e]);
+          } else {
+            buf[r * pitch + i * 16 + g] = o[i][e];
+            buf[r * pitch + i * 16 + 8 + g] = o[i][2 + e];
+          }
+        }
+      }
+    }
+  }
+};
+
+// The same for 16 * MT rows, which fill M themselves: S = Q K^T, O = P V, and
+// P is already in the second product's operand layout.  A lane holds rows g,
+// g + 8 of a tile and keys 2 c4, 2 c4 + 1 of each group of eight.  (Keys on M
+// cost these 12 % more time: a transpose for every eight weights.)
+template <int D, int CT, int KS, int MT>
+struct RowsOnM {
+  static constexpr bool F8 = CT == IDX_E4M3, MB = CT == IDX_BF16;
+  static constexpr int ROWB = row_bytes<D, CT>();
+  float o[MT][D / 8][4], s[MT][KS / 8][4], m[MT][2], l[MT][2];
+
+  struct Factors {
+    float f[MT][2];
+  };
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void load_q(uint32_t, int) {}
+  __device__ __forceinline__ void scores(uint32_t kt, uint32_t q_u, int lane) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < KS / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+#pragma unroll
+    for (int k2 = 0; k2 < D / 32; ++k2) {
+      uint32_t qa[2][MT][4];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          ldsm4(q_u + swz<D * 2>(mt * 16 + (lane & 15), 4 * k2 + 2 * ks + (lane >> 4)), qa[ks][mt]);
+#pragma unroll
+      for (int kg = 0; kg < KS / 16; ++kg) {
+        uint32_t kb[2][4];  // per k16 step: operand pairs of two groups of eight keys
+        if (F8) {
+          uint32_t r[4];
+          ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 2 * k2 + (lane >> 4)), r);
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              kb[ks][2 * n] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + n] & 0xFFFF));
+              kb[ks][2 * n + 1] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + n] >> 16));
+            }
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                 4 * k2 + 2 * ks + ((lane >> 3) & 1)), kb[ks]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+              mma16816<MB>(s[mt][2 * kg + n], qa[ks][mt], kb[ks][2 * n], kb[ks][2 * n + 1]);
+      }
+    }
+  }
+  __device__ __forceinline__ Factors factors(const float* mult, int lane) const {
+    Factors f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) f.f[mt][e] = mult[mt * 16 + (lane >> 2) + 8 * e];
+    return f;
+  }
+  __device__ __forceinline__ void cap(float softcap, const float* mult, int lane) {
+    const Factors f = factors(mult, lane);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < KS / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          s[mt][i][e] = softcap * kLog2e * tanhf(s[mt][i][e] * f.f[mt][e >> 1]);
+  }
+  __device__ __forceinline__ void mask(const Sight& v, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int i = 0; i < KS / 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int kk = i * 8 + 2 * c4 + k;
+        const bool there = v.there(kk);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (!there || !v.in(kk, mt * 16 + g + 8 * e)) s[mt][i][2 * e + k] = -INFINITY;
+      }
+  }
+  __device__ __forceinline__ void values(uint32_t vt, const Factors& f, int lane) {
+    float mx[MT][2];
+    bool raise = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = fmaxf(s[mt][0][2 * e], s[mt][0][2 * e + 1]);
+#pragma unroll
+        for (int i = 1; i < KS / 8; ++i) x = fmaxf(x, fmaxf(s[mt][i][2 * e], s[mt][i][2 * e + 1]));
+        mx[mt][e] = x * f.f[mt][e];
+        raise = raise || mx[mt][e] > m[mt][e] + kSlack;
+      }
+    if (__any_sync(~0u, raise)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(mx[mt][e], m[mt][e]);
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+          const float w = m[mt][e] == -INFINITY ? 0.f : ex2(m[mt][e] - x);
+          m[mt][e] = x;
+          l[mt][e] *= w;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            o[mt][i][2 * e] *= w;
+            o[mt][i][2 * e + 1] *= w;
+          }
+        }
+    }
+#pragma unroll
+    for (int kg = 0; kg < KS / 16; ++kg) {
+      uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float r = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = ex2(fmaf(s[mt][2 * kg + n][2 * e], f.f[mt][e], r));
+            const float p1 = ex2(fmaf(s[mt][2 * kg + n][2 * e + 1], f.f[mt][e], r));
+            l[mt][e] += p0 + p1;
+            two_terms<MB>(p0, p1, &ph[mt][2 * n + e], &pl[mt][2 * n + e]);
+          }
+        }
+      if (F8) {
+        // dimensions 2n, 2n + 1 of a 16-block: even ones feed one product, odd the next
+#pragma unroll
+        for (int db = 0; db < D / 32; ++db) {
+          uint32_t r[4];
+          ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), r);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t w0 = __byte_perm(r[2 * hf], 0, 0x3120);
+            const uint32_t w1 = __byte_perm(r[2 * hf + 1], 0, 0x3120);
+            const uint32_t e0 = e4m3x2_to_f16x2((uint16_t)(w0 & 0xFFFF));
+            const uint32_t e1 = e4m3x2_to_f16x2((uint16_t)(w1 & 0xFFFF));
+            const uint32_t o0 = e4m3x2_to_f16x2((uint16_t)(w0 >> 16));
+            const uint32_t o1 = e4m3x2_to_f16x2((uint16_t)(w1 >> 16));
+            const int i = (2 * db + hf) * 2;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816<MB>(o[mt][i], ph[mt], e0, e1);
+              mma16816<MB>(o[mt][i + 1], ph[mt], o0, o1);
+              mma16816<MB>(o[mt][i], pl[mt], e0, e1);
+              mma16816<MB>(o[mt][i + 1], pl[mt], o0, o1);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int db = 0; db < D / 16; ++db) {
+          uint32_t vb[4];
+          ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), vb);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816<MB>(o[mt][2 * db], ph[mt], vb[0], vb[1]);
+            mma16816<MB>(o[mt][2 * db + 1], ph[mt], vb[2], vb[3]);
+            mma16816<MB>(o[mt][2 * db], pl[mt], vb[0], vb[1]);
+            mma16816<MB>(o[mt][2 * db + 1], pl[mt], vb[2], vb[3]);
+          }
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void leave(float* buf, int pitch, float2* ml, int rows, int lane) {
+    const int g = lane >> 2, c4 = lane & 3;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = mt * 16 + g + 8 * e;
+        float x = l[mt][e];
+        x += __shfl_xor_sync(~0u, x, 1);
+        x += __shfl_xor_sync(~0u, x, 2);
+        if (r < rows) {
+          if (c4 == 0) ml[r] = make_float2(m[mt][e], x);
+          float* row = buf + r * pitch;
+#pragma unroll
+          for (int i = 0; i < D / 8; i += 2) {
+            if (F8) {
+              *reinterpret_cast<float4*>(row + i * 8 + 4 * c4) =
+                  make_float4(o[mt][i][2 * e], o[mt][i + 1][2 * e], o[mt][i][2 * e + 1],
+                              o[mt][i + 1][2 * e + 1]);
+            } else {
+              *reinterpret_cast<float2*>(row + i * 8 + 2 * c4) =
+                  make_float2(o[mt][i][2 * e], o[mt][i][2 * e + 1]);
+              *reinterpret_cast<float2*>(row + i * 8 + 8 + 2 * c4) =
+                  make_float2(o[mt][i + 1][2 * e], o[mt][i + 1][2 * e + 1]);
+            }
+          }
+        }
+      }
+  }
+};
+
+template <int D, int CT, int NT, int KS>
+struct TileOf {
+  using type = RowsOnM<D, CT, KS, NT / 2>;
+};
+template <int D, int CT, int KS>
+struct TileOf<D, CT, 1, KS> {
+  using type = KeysOnM<D, CT, KS>;
+};
+
 // A request as an item sees it.
 struct Span {
   int len;    // clamped context
@@ -203,7 +655,9 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   __shared__ long long s_warp[kWarps];
   __shared__ long long s_base;
   __shared__ int s_req, s_seg;
-  __shared__ float s_mult[C::kRows];
+  // log2 score per product (with a cap: its argument), and ones for capped scores
+  __shared__ __align__(8) float s_mult[C::kRows], s_one[C::kRows];
+  __shared__ int s_end[C::kRows];  // first key past a row's sight
   __shared__ float2 s_ml[kWarps][C::kRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t* ring = smem + warp * C::kRing;
@@ -249,7 +703,6 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
     }
   }
   const Cut cut(a.split ? U : (long long)gridDim.x, (int)gridDim.x);
-  const int g = lane >> 2, c4 = lane & 3;  // fragment row and column group
   const bool use_cap = a.softcap > 0.f;
 
   for (int seg = blockIdx.x; seg < cut.segments();) {
@@ -346,17 +799,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
 
-      float o[NT][D / 16][4];
-      float m[NT][2], l[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][i][e] = 0.f;
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
-      }
+      typename TileOf<D, CT, NT, KS>::type tile;
+      tile.clear();
 
       // units whose page groups of 16 keys (or listed positions) fit the table
       const int sub = tab_words / (listed ? C::kUnit : C::kUnit / 16);
@@ -427,6 +871,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
               if (part == 0) {
                 // a masked score (-inf) times the factor must stay one: at least FLT_MIN
                 s_mult[r] = use_cap ? mult / a.softcap : fmaxf(mult * kLog2e, FLT_MIN);
+                s_one[r] = 1.f;
+                s_end[r] = end0 + (row0 + r) / a.group;
               }
               // a negative scale is carried by the queries, so that the factor is not negative
               const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
@@ -473,13 +919,21 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
                 const uint32_t e = tb_[grp];
                 const int key = (sp.t0 + sa) * C::kUnit + grp * 16 + rl;
                 const uint8_t* src = src0 + (e != kNone ? (uint64_t)e * a.off_unit + rl * ts : 0);
-                // rows of the group that some query sees: [from, to)
-                const int from = e != kNone ? lo_all - key : 16, to = sp.len - key;
+                if (e != kNone && key - rl >= lo_all && key - rl + 16 <= sp.len) {
 #pragma unroll
-                for (int j = 0; j < 16 / RPI; ++j) {
-                  const bool ok = j * RPI >= from && j * RPI < to;
-                  cp_async_16_zfill(dst + swz<ROWB>(gr * 16 + j * RPI + rl, cl), ok ? src : src0, ok);
-                  src += RPI * ts;
+                  for (int j = 0; j < 16 / RPI; ++j) {
+                    cp_async_16(dst + swz<ROWB>(gr * 16 + j * RPI + rl, cl), src);
+                    src += RPI * ts;
+                  }
+                } else {
+                  // rows of the group that some query sees: [from, to)
+                  const int from = e != kNone ? lo_all - key : 16, to = sp.len - key;
+#pragma unroll
+                  for (int j = 0; j < 16 / RPI; ++j) {
+                    const bool ok = j * RPI >= from && j * RPI < to;
+                    cp_async_16_zfill(dst + swz<ROWB>(gr * 16 + j * RPI + rl, cl), ok ? src : src0, ok);
+                    src += RPI * ts;
+                  }
                 }
               }
             }
@@ -490,96 +944,15 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < NS; ++i) issue(i);
 
-        float mult[NT][2];
-        int end[NT][2];  // first key past the row's sight
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            mult[nt][e] = s_mult[nt * 8 + 2 * c4 + e];
-            end[nt][e] = end0 + (row0 + nt * 8 + 2 * c4 + e) / a.group;
-          }
-        uint32_t qf[C::kQRegs ? D / 8 : 1];
-        if (C::kQRegs) {
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t r[4];
-            ldsm4(q_u + swz<D * 2>(lane & 7, 4 * i + (lane >> 3)), r);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) qf[4 * i + j] = r[j];
-          }
-        }
-
+        tile.load_q(q_u, lane);
         for (int t = 0; t < sb - sa; ++t) {
-          // ---- scores of KS keys
-          float s[KS / 16][NT][4];
-#pragma unroll
-          for (int kg = 0; kg < KS / 16; ++kg)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) s[kg][nt][e] = 0.f;
           cp_async_wait_group<NS - 1>();
           __syncwarp();
-          {
-            const uint32_t kt = ring_u + get * C::kHalf;
-#pragma unroll
-            for (int k2 = 0; k2 < D / 32; ++k2) {  // 32 dimensions at a time
-              uint32_t qb[2][NT][2];
-              if (C::kQRegs) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) qb[j >> 1][0][j & 1] = qf[4 * k2 + j];
-              } else if (NT == 1) {
-                uint32_t r[4];
-                ldsm4(q_u + swz<D * 2>(lane & 7, 4 * k2 + (lane >> 3)), r);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) qb[j >> 1][0][j & 1] = r[j];
-              } else {
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                  for (int n2 = 0; n2 < NT / 2; ++n2) {
-                    uint32_t r[4];
-                    ldsm4(q_u + swz<D * 2>(n2 * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                           4 * k2 + 2 * ks + ((lane >> 3) & 1)), r);
-                    qb[ks][2 * n2][0] = r[0];
-                    qb[ks][2 * n2][1] = r[1];
-                    qb[ks][2 * n2 + 1][0] = r[2];
-                    qb[ks][2 * n2 + 1][1] = r[3];
-                  }
-              }
-#pragma unroll
-              for (int kg = 0; kg < KS / 16; ++kg) {
-                uint32_t ka[2][4];
-                if (F8) {
-                  // one matrix: 8 keys x 16 codes; a lane's four codes are its operand
-                  // values of both halves of a k16 step
-                  uint32_t r[4];
-                  ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 2 * k2 + (lane >> 4)), r);
-#pragma unroll
-                  for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                      ka[ks][hf] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + hf] & 0xFFFF));
-                      ka[ks][2 + hf] = e4m3x2_to_f16x2((uint16_t)(r[2 * ks + hf] >> 16));
-                    }
-                } else {
-#pragma unroll
-                  for (int ks = 0; ks < 2; ++ks)
-                    ldsm4(kt + swz<ROWB>(kg * 16 + (lane & 15), 4 * k2 + 2 * ks + (lane >> 4)), ka[ks]);
-                }
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) mma16816<MB>(s[kg][nt], ka[ks], qb[ks][nt][0], qb[ks][nt][1]);
-              }
-            }
-          }
+          tile.scores(ring_u + get * C::kHalf, q_u, lane);
           __syncwarp();
           get = get + 1 == NS ? 0 : get + 1;
           issue(2 * t + NS);
 
-          // ---- capped and masked (a lane holds keys g, g + 8 of a group, rows 2 c4, 2 c4 + 1)
           const int tile0 = t * C::kUnit + warp * KS;  // within the sub-range
           const int key0 = (sp.t0 + sa) * C::kUnit + tile0;
           bool whole;  // every key of the tile is seen by every row
@@ -594,135 +967,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             whole = ok && key0 + KS <= end0 &&
                     (a.window == 0 || key0 >= end0 + n_tok - 1 - a.window);
           }
-          if (use_cap) {
-#pragma unroll
-            for (int kg = 0; kg < KS / 16; ++kg)
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  s[kg][nt][e] = a.softcap * kLog2e * tanhf(s[kg][nt][e] * mult[nt][e & 1]);
-          }
-          if (!whole) {
-#pragma unroll
-            for (int kg = 0; kg < KS / 16; ++kg)
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const int kk = kg * 16 + hf * 8 + g;
-                const bool there = tab[listed ? tile0 + kk : (tile0 + kk) / 16] != kNone;
-                const int key = key0 + kk;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const bool seen = there && (listed || (key < end[nt][e] &&
-                                                           (a.window == 0 || key >= end[nt][e] - a.window)));
-                    if (!seen) s[kg][nt][2 * hf + e] = -INFINITY;
-                  }
-              }
-          }
-          // log2 scores are x * f with f = 1 where the cap has been applied
-          float mx[NT][2];
-          bool raise = false;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
-#pragma unroll
-              for (int kg = 1; kg < KS / 16; ++kg) x = fmaxf(x, fmaxf(s[kg][nt][e], s[kg][nt][2 + e]));
-              mx[nt][e] = use_cap ? x : x * mult[nt][e];
-              raise = raise || mx[nt][e] > m[nt][e] + kSlack;
-            }
-          if (__any_sync(~0u, raise)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(mx[nt][e], m[nt][e]);
-                x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-                const float f = m[nt][e] == -INFINITY ? 0.f : ex2(m[nt][e] - x);
-                m[nt][e] = x;
-                l[nt][e] *= f;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                  o[nt][i][e] *= f;
-                  o[nt][i][2 + e] *= f;
-                }
-              }
-          }
-          // ---- weights, as two 16-bit terms in the second product's operand layout
-          uint32_t ph[KS / 16][NT][2], pl[KS / 16][NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float f[2], r[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              f[e] = use_cap ? 1.f : mult[nt][e];
-              r[e] = m[nt][e] == -INFINITY ? 0.f : -m[nt][e];
-            }
-#pragma unroll
-            for (int kg = 0; kg < KS / 16; ++kg)
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const float p0 = ex2(fmaf(s[kg][nt][2 * hf], f[0], r[0]));
-                const float p1 = ex2(fmaf(s[kg][nt][2 * hf + 1], f[1], r[1]));
-                l[nt][0] += p0;
-                l[nt][1] += p1;
-                const uint32_t hi = pack2<MB>(p0, p1);
-                const float2 back = unpack2<MB>(hi);
-                ph[kg][nt][hf] = transpose8x8(hi);
-                pl[kg][nt][hf] = transpose8x8(pack2<MB>(p0 - back.x, p1 - back.y));
-              }
-          }
+          if (use_cap) tile.cap(a.softcap, s_mult, lane);
+          if (!whole) tile.mask(Sight{tab, s_end, tile0, key0, a.window, listed}, lane);
 
-          // ---- weighted sum of the values
           cp_async_wait_group<NS - 1>();
           __syncwarp();
-          {
-            const uint32_t vt = ring_u + get * C::kHalf;
-#pragma unroll
-            for (int kg = 0; kg < KS / 16; ++kg) {
-              if (F8) {
-                // a matrix of 8 keys x 16 codes transposed gives a lane two keys' codes at
-                // dimensions 2g, 2g+1: the even one is row g of the operand, the odd g + 8
-#pragma unroll
-                for (int db = 0; db < D / 32; ++db) {
-                  uint32_t r[4];
-                  ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 15), 2 * db + (lane >> 4)), r);
-#pragma unroll
-                  for (int hf = 0; hf < 2; ++hf) {
-                    uint32_t va[4];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                      const uint32_t w = __byte_perm(r[2 * hf + j], 0, 0x3120);
-                      va[2 * j] = e4m3x2_to_f16x2((uint16_t)(w & 0xFFFF));
-                      va[2 * j + 1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                      mma16816<MB>(o[nt][2 * db + hf], va, ph[kg][nt][0], ph[kg][nt][1]);
-                      mma16816<MB>(o[nt][2 * db + hf], va, pl[kg][nt][0], pl[kg][nt][1]);
-                    }
-                  }
-                }
-              } else {
-#pragma unroll
-                for (int db = 0; db < D / 16; ++db) {
-                  uint32_t va[4];
-                  ldsm4t(vt + swz<ROWB>(kg * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                        2 * db + ((lane >> 3) & 1)), va);
-#pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    mma16816<MB>(o[nt][db], va, ph[kg][nt][0], ph[kg][nt][1]);
-                    mma16816<MB>(o[nt][db], va, pl[kg][nt][0], pl[kg][nt][1]);
-                  }
-                }
-              }
-            }
-          }
+          tile.values(ring_u + get * C::kHalf, tile.factors(use_cap ? s_one : s_mult, lane), lane);
           __syncwarp();
           get = get + 1 == NS ? 0 : get + 1;
           issue(2 * t + 1 + NS);
@@ -732,32 +982,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       }
 
       // ---- the warps' sums become one: each leaves its own in its ring
-      {
-        float* buf = reinterpret_cast<float*>(ring);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = nt * 8 + 2 * c4 + e;
-            float s = l[nt][e];
-            s += __shfl_xor_sync(~0u, s, 4);
-            s += __shfl_xor_sync(~0u, s, 8);
-            s += __shfl_xor_sync(~0u, s, 16);
-            if (r < rows) {
-              if (g == 0) s_ml[warp][r] = make_float2(m[nt][e], s);
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                if (F8) {
-                  *reinterpret_cast<float2*>(buf + r * C::kPitch + i * 16 + 2 * g) =
-                      make_float2(o[nt][i][e], o[nt][i][2 + e]);
-                } else {
-                  buf[r * C::kPitch + i * 16 + g] = o[nt][i][e];
-                  buf[r * C::kPitch + i * 16 + 8 + g] = o[nt][i][2 + e];
-                }
-              }
-            }
-          }
-      }
+      tile.leave(reinterpret_cast<float*>(ring), C::kPitch, s_ml[warp], rows, lane);
       const bool last_item = u + (tb - ta) >= u1;
       if (last_item && a.split && cut.K > 0 && tid == 0) {
         // the next segment, claimed while the sums are joined
