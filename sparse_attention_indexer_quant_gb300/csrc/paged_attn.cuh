@@ -146,10 +146,10 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   return (uint32_t)(r * ROWB + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-__device__ __forceinline__ long long warp_incl_sum(long long x, int lane) {
+__device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(~0u, x, d);
+    const int y = __shfl_up_sync(~0u, x, d);
     if (lane >= d) x += y;
   }
   return x;
@@ -158,35 +158,45 @@ __device__ __forceinline__ long long warp_incl_sum(long long x, int lane) {
 // The cut of U units into segments by R CTAs.  One level of A = min(R, U)
 // equal segments, or K + 1 levels of R: 3/4 of the units, then 1/8, 1/16, ...,
 // 2^-(K+1), 2^-(K+1), as far as the smallest segments keep kMinSegment units.
+// Segments weigh whole 2^-(K+1) / R parts of the units, the first `rem` parts
+// one unit more than the others.
 constexpr int kMinSegment = 3;
 struct Cut {
-  long long U;
-  int R, K;
-  __device__ Cut(long long units, int ctas) : U(units), R(ctas), K(0) {
+  int R, K, U, part, rem;
+  __device__ Cut(int units, int ctas) : R(ctas), K(0), U(units) {
 #pragma unroll
     for (int k = 2; k < kAttnLevels; ++k)
-      if (U >= (long long)kMinSegment * R << (k + 1)) K = k;
-    if (K == 0 && R > U) R = (int)U;
+      if (U >> (k + 1) >= kMinSegment * R) K = k;
+    if (K == 0 && R > U) R = U;
+    const int parts = K == 0 ? R : R << (K + 1);
+    part = U / parts;
+    rem = U - part * parts;
   }
   __device__ int segments() const { return R * (K + 1); }
-  // weight of one segment of level l, and of all segments before level l (per CTA)
-  __device__ int weight(int l) const { return K == 0 ? 1 : (l == 0 ? 3 << (K - 1) : (l < K ? 1 << (K - 1 - l) : 1)); }
+  // parts of one segment of level l, and of all segments before level l (per CTA)
+  __device__ int weight(int l) const { return l == 0 ? (K == 0 ? 1 : 3 << (K - 1)) : (l < K ? 1 << (K - 1 - l) : 1); }
   __device__ int before(int l) const { return l == 0 ? 0 : (2 << K) - (1 << (K - l)); }
-  __device__ long long total() const { return K == 0 ? R : (long long)R << (K + 1); }
   // first unit of segment s (s = segments(): U)
-  __device__ long long start(int s) const {
-    const int l = s / R, i = s - l * R;
+  __device__ int start(int s) const {
+    const int l = s / R;
     if (l > K) return U;
-    return ((long long)R * before(l) + (long long)i * weight(l)) * U / total();
+    const int x = R * before(l) + (s - l * R) * weight(l);
+    return x * part + min(x, rem);
   }
   // the segment that holds unit u
-  __device__ int owner(long long u) const {
-    const long long x = ((u + 1) * total() + U - 1) / U;  // least weight sum past u
+  __device__ int owner(int u) const {
+    const int x = u < rem * (part + 1) ? u / (part + 1) : rem + (u - rem * (part + 1)) / part;
     int l = 0;
-    while (l < K && x > (long long)R * before(l + 1)) ++l;
-    const int w = weight(l);
-    return l * R + (int)((x - (long long)R * before(l) + w - 1) / w) - 1;
+    while (l < K && x >= R * before(l + 1)) ++l;
+    return l * R + (x - R * before(l)) / weight(l);
   }
+};
+
+// A request as an item sees it.
+struct Span {
+  int len;    // clamped context
+  int t0;     // first unit of its keys
+  int units;  // units (at least one, so that an empty request's rows are written)
 };
 
 // What a tile's masking goes by: key kk of the tile (keys key0 ..) is seen by
@@ -638,13 +648,6 @@ struct TileOf<D, CT, 1, KS> {
   using type = KeysOnM<D, CT, KS>;
 };
 
-// A request as an item sees it.
-struct Span {
-  int len;    // clamped context
-  int t0;     // first unit of its keys
-  int units;  // units (at least one, so that an empty request's rows are written)
-};
-
 template <int D, int CT, int NT>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, CT, NT>::kOcc))
 paged_attn_kernel(const __grid_constant__ AttnArgs a) {
@@ -652,9 +655,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   constexpr bool F8 = C::kF8, MB = C::kMmaBf16;
   constexpr int KS = C::kKS, ROWB = C::kRowB, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ long long s_warp[kWarps];
-  __shared__ long long s_base;
-  __shared__ int s_req, s_seg;
+  __shared__ int s_warp[kWarps];
+  __shared__ int s_base, s_req, s_seg;
   // log2 score per product (with a cap: its argument), and ones for capped scores
   __shared__ __align__(8) float s_mult[C::kRows], s_one[C::kRows];
   __shared__ int s_end[C::kRows];  // first key past a row's sight
@@ -687,12 +689,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 
   const int reqs = listed ? a.B * a.next_n : a.B;
   const int list_units = (a.topk + C::kUnit - 1) / C::kUnit;
-  long long U = 0;
+  int U = 0;  // below 2^31, as the caller has checked
   if (a.split) {
     if (listed) {
-      U = (long long)reqs * HR * list_units;
+      U = reqs * HR * list_units;
     } else {
-      long long sum = 0;
+      int sum = 0;
       for (int b = tid; b < reqs; b += kThreads) sum += span_of(b).units;
       sum = warp_incl_sum(sum, lane);
       if (lane == 31) s_warp[warp] = sum;
@@ -702,41 +704,42 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       U *= HR;
     }
   }
-  const Cut cut(a.split ? U : (long long)gridDim.x, (int)gridDim.x);
+  const Cut cut(a.split ? U : (int)gridDim.x, (int)gridDim.x);
+  // every CTA is running: the join may take the room of those that finish first
+  pdl_launch_dependents();
   const bool use_cap = a.softcap > 0.f;
 
   for (int seg = blockIdx.x; seg < cut.segments();) {
     // ---- the segment's units [u0, u1), and the request its first unit belongs to
-    long long u0, u1, base;  // base: first unit of request `req`
-    int req;
+    int u0, u1, base, req;  // base: first unit of request `req`
     if (!a.split) {  // one CTA per item; units are counted from its request's first
       const int units = listed ? list_units : span_of(seg / HR).units;
       req = seg / HR;
       base = 0;
-      u0 = (long long)(seg % HR) * units;
+      u0 = (seg % HR) * units;
       u1 = u0 + units;
     } else {
       u0 = cut.start(seg);
       u1 = cut.start(seg + 1);
       if (listed) {
-        req = (int)(u0 / ((long long)HR * list_units));
-        base = (long long)req * HR * list_units;
+        req = u0 / (HR * list_units);
+        base = req * HR * list_units;
       } else {
-        long long before = 0;  // units of the requests before this round's
+        int before = 0;  // units of the requests before this round's
         for (int b0 = 0;; b0 += kThreads) {
           const int b = b0 + tid;
-          const long long mine = b < reqs ? (long long)span_of(b).units * HR : 0;
-          long long incl = warp_incl_sum(mine, lane);
+          const int mine = b < reqs ? span_of(b).units * HR : 0;
+          int incl = warp_incl_sum(mine, lane);
           __syncthreads();
           if (lane == 31) s_warp[warp] = incl;
           __syncthreads();
-          long long total = 0;
+          int total = 0;
 #pragma unroll
           for (int w = 0; w < kWarps; ++w) {
             if (w < warp) incl += s_warp[w];
             total += s_warp[w];
           }
-          const long long first = before + incl - mine;
+          const int first = before + incl - mine;
           if (mine > 0 && first <= u0 && u0 < first + mine) {
             s_req = b;
             s_base = first;
@@ -750,17 +753,17 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       }
     }
 
-    for (long long u = u0; u < u1;) {
+    for (int u = u0; u < u1;) {
       // ---- the item at unit u, and the part of it that is this segment's
       const int b = listed ? req / a.next_n : req;
       const int tok0 = listed ? req : req * a.next_n;  // query row of the item's first row
       const int n_tok = listed ? 1 : a.next_n;
       const Span sp = span_of(b);
       const int units = listed ? list_units : sp.units;
-      const int hr = (int)((u - base) / units);
+      const int hr = (u - base) / units;
       const int h = hr / a.row_tiles, rt = hr % a.row_tiles;
-      const int ta = (int)((u - base) - (long long)hr * units);
-      const int tb = (int)min((long long)units, ta + (u1 - u));
+      const int ta = u - base - hr * units;
+      const int tb = min(units, ta + (u1 - u));
       const int row0 = rt * C::kRows;
       const int rows = min(C::kRows, a.rows - row0);
       constexpr int EB = F8 ? 1 : 2;  // bytes of a cached value
@@ -995,7 +998,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       // first segment's last (or only) part, then the following segments' first parts
       const int part = 2 * seg + (u == u0 ? 0 : 1);
       if (a.split && ta == 0 && tid == 0)
-        a.desc[(long long)req * HR + hr] = make_int2(part, cut.owner(u + units - 1) - seg + 1);
+        a.desc[req * HR + hr] = make_int2(part, cut.owner(u + units - 1) - seg + 1);
       constexpr int QPR = D / 4;  // float4 quads per row
       for (int i = tid; i < rows * QPR; i += kThreads) {
         const int r = i / QPR, d = (i % QPR) * 4;
@@ -1040,15 +1043,14 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       __syncthreads();  // the rings, the table and the query rows are refilled next
 
       u += tb - ta;
-      if (u - base >= (long long)units * HR) {
-        base += (long long)units * HR;
+      if (u - base >= units * HR) {
+        base += units * HR;
         ++req;
       }
     }
     if (!a.split || cut.K == 0) break;
     seg = s_seg;
   }
-  pdl_launch_dependents();
 }
 
 template <int D, int CT, int NT>

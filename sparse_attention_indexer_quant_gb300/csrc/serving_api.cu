@@ -424,7 +424,9 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
   a.split = units > 2;
   const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
-  if (grid > INT32_MAX) return fail(IDX_ERR_INVALID_ARG, "too many query rows");
+  if (units * items > INT32_MAX || items * a.part_rows > INT32_MAX)
+    return fail(IDX_ERR_INVALID_ARG, "%lld query row tiles of up to %lld keys: too much for one call",
+                (long long)items, (long long)keys);
   a.grid = (int32_t)grid;
   cudaError_t e = kv->dtype == IDX_BF16   ? idx::launch_attn_bf16(a, (cudaStream_t)stream)
                   : kv->dtype == IDX_FP16 ? idx::launch_attn_fp16(a, (cudaStream_t)stream)
