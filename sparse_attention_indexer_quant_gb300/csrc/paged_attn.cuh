@@ -160,7 +160,7 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 // 2^-(K+1), 2^-(K+1), as far as the smallest segments keep kMinSegment units.
 // Segments weigh whole 2^-(K+1) / R parts of the units, the first `rem` parts
 // one unit more than the others.
-constexpr int kMinSegment = 3;
+constexpr int kMinSegment = 5;
 struct Cut {
   int R, K, U, part, rem;
   __device__ Cut(int units, int ctas) : R(ctas), K(0), U(units) {
@@ -810,38 +810,54 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       for (int sa = ta; sa < tb; sa += sub) {
         const int sb = min(tb, sa + sub);
         if (sa > ta) __syncthreads();  // the previous range's table is done with
+        // four entries at a time, their loads issued together (a list entry and
+        // then its page id are two dependent round trips)
+        constexpr int TB = 4;
         if (listed) {
           const int* list = a.topk_idx + (int64_t)req * a.topk;
           const int my_end = max(0, sp.len - a.next_n + 1 + req % a.next_n);
-          for (int i = tid; i < (sb - sa) * C::kUnit; i += kThreads) {
-            const int at = sa * C::kUnit + i;
-            const int p = at < a.topk ? __ldg(list + at) : -1;
-            int id = -1;
-            if (p >= 0) {
-              if (p < my_end) {
-                id = __ldg(bt + (p >> a.page_shift));
-                if (id >= a.kv.num_blocks) id = -1;
-              }
-              if (id < 0 && hr == 0) count_bad_input(a.errors);
+          const int n = (sb - sa) * C::kUnit;
+          for (int i0 = tid; i0 < n; i0 += TB * kThreads) {
+            int p[TB], id[TB];
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+              const int i = i0 + j * kThreads, at = sa * C::kUnit + i;
+              p[j] = i < n && at < a.topk ? __ldg(list + at) : -1;
             }
-            tab[i] = id < 0 ? kNone : k_off(id, p & page_mask);
-            if (!a.one_table) vtab[i] = id < 0 ? kNone : v_off(id, p & page_mask);
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+              id[j] = p[j] >= 0 && p[j] < my_end ? __ldg(bt + (p[j] >> a.page_shift)) : -1;
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+              const int i = i0 + j * kThreads;
+              if (i >= n) break;
+              const bool ok = id[j] >= 0 && id[j] < a.kv.num_blocks;
+              if (!ok && p[j] >= 0 && hr == 0) count_bad_input(a.errors);
+              tab[i] = ok ? k_off(id[j], p[j] & page_mask) : kNone;
+              if (!a.one_table) vtab[i] = ok ? v_off(id[j], p[j] & page_mask) : kNone;
+            }
           }
         } else {
-          const int g0 = (sp.t0 + sa) * (C::kUnit / 16), ng = (sb - sa) * (C::kUnit / 16);
-          for (int i = tid; i < ng; i += kThreads) {
-            const int key = (g0 + i) * 16;
-            int id = -1;
-            if (key < sp.len && key + 16 > lo_all) {
-              id = __ldg(bt + (key >> a.page_shift));
-              if (id < 0 || id >= a.kv.num_blocks) {
-                // counted once per page, by its first group that is in sight
-                if (hr == 0 && ((key & page_mask) == 0 || key <= lo_all)) count_bad_input(a.errors);
-                id = -1;
-              }
+          const int g0 = (sp.t0 + sa) * (C::kUnit / 16), n = (sb - sa) * (C::kUnit / 16);
+          for (int i0 = tid; i0 < n; i0 += TB * kThreads) {
+            int id[TB];
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+              const int i = i0 + j * kThreads, key = (g0 + i) * 16;
+              id[j] = i < n && key < sp.len && key + 16 > lo_all ? __ldg(bt + (key >> a.page_shift)) : -1;
             }
-            tab[i] = id < 0 ? kNone : k_off(id, key & page_mask);
-            if (!a.one_table) vtab[i] = id < 0 ? kNone : v_off(id, key & page_mask);
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+              const int i = i0 + j * kThreads, key = (g0 + i) * 16;
+              if (i >= n) break;
+              const bool ok = id[j] >= 0 && id[j] < a.kv.num_blocks;
+              // counted once per page, by its first group that is in sight
+              if (!ok && key < sp.len && key + 16 > lo_all && hr == 0 &&
+                  ((key & page_mask) == 0 || key <= lo_all))
+                count_bad_input(a.errors);
+              tab[i] = ok ? k_off(id[j], key & page_mask) : kNone;
+              if (!a.one_table) vtab[i] = ok ? v_off(id[j], key & page_mask) : kNone;
+            }
           }
         }
         if (sa == ta) {

@@ -304,6 +304,28 @@ def test_insert_keeps_infinities_in_their_dimension(idx):
         assert torch.equal(out, q) and torch.equal(kc[0, 0, 0], q[0, 0]) and torch.equal(vc, kc)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_insert_takes_tables_and_weights_at_any_address(idx, inter):
+    """4-byte aligned tables and weights give the same bytes as aligned ones."""
+    q = torch.randn(37, 3, 128, device="cuda").bfloat16()
+    cos, sin, w = torch.rand(50, 32, device="cuda"), torch.rand(50, 32, device="cuda"), torch.rand(128, device="cuda")
+
+    def off(t):
+        buf = torch.empty(t.numel() + 1, device="cuda")
+        buf[1:].copy_(t.flatten())
+        return buf[1:].view(t.shape)
+
+    pos, slots = i32(np.arange(37) % 50), torch.arange(37, device="cuda")
+    got = []
+    for f in (lambda t: t, off):
+        kc, vc = idx.new_kv_cache(3, 3, 128, page_size=16)
+        out = idx.qk_norm_rope_insert(q, q, q, f(w), f(w), 1e-6, pos, f(cos), f(sin), 64, slots, kc,
+                                      vc, interleaved=inter)
+        got.append((out, kc, vc))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 def test_insert_on_another_stream(idx):
     s = torch.cuda.Stream()
     q = torch.randn(64, 8, 128, device="cuda").bfloat16()
