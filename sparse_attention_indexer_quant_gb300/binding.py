@@ -450,22 +450,35 @@ def copy_async(dst: torch.Tensor, src: torch.Tensor, stream=None) -> None:
 
 # ---------------------------------------------------------------- serving operators
 
-DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
 ROPE_SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
-
-
-def _empty(shape, dtype, device, stream):
-    """torch.empty for a call on `stream`: its memory belongs to that stream, so
-    it can neither be taken from work still pending on the current one nor be
-    reused before the call is done."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
 
 StepPlan = collections.namedtuple(
     "StepPlan", "context_lens query_start slot_mapping positions token_seq pool_head")
+
+
+def _load_serving():
+    try:
+        from . import _serving
+    except ImportError as e:
+        raise RuntimeError(
+            "the serving binding is missing or does not load: build it first "
+            "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    _serving.set_errors(IdxError, torch.OutOfMemoryError)
+    return _serving
+
+
+# Checks, allocation and marshalling of the serving entries (csrc/serving_py.cpp).
+# Outputs and workspaces are allocated on the stream of the call: their memory
+# can then neither be taken from work still pending on another stream nor be
+# reused before the call is done.
+_serving = _load_serving()
+
+
+def _call(fn, stream, *args):
+    if stream is None:
+        return fn(*args)
+    with torch.cuda.stream(stream):
+        return fn(*args)
 
 
 def plan_step(cached_lens, new_lens, block_table, free_pages, pool_head, num_tokens: int,
@@ -480,47 +493,14 @@ def plan_step(cached_lens, new_lens, block_table, free_pages, pool_head, num_tok
     token_seq [num_tokens], and the advanced pool_head [1] (all int32 but the
     slots); num_tokens may exceed the step's tokens (slot -1, position 0 and
     request -1 past them).  `out`: an earlier plan to write into."""
-    for t, name in ((cached_lens, "cached_lens"), (new_lens, "new_lens"),
-                    (block_table, "block_table"), (free_pages, "free_pages"),
-                    (pool_head, "pool_head")):
-        _need(t, torch.int32, name)
-    B = cached_lens.numel()
-    if new_lens.numel() != B:
-        raise ValueError("cached_lens and new_lens must have one entry per request")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_blocks]")
-    if pool_head.numel() != 1:
-        raise ValueError("pool_head must hold one value")
-    if out is None:
-        dev = cached_lens.device
-        # one allocation for the int32 arrays
-        flat = _empty(2 * B + 2 + 2 * max(num_tokens, 0), torch.int32, dev, stream)
-        ctx, start, head, pos, seq = flat.split((B, B + 1, 1, max(num_tokens, 0), max(num_tokens, 0)))
-        out = StepPlan(ctx, start, _empty(max(num_tokens, 0), torch.int64, dev, stream), pos, seq,
-                       head)
-    else:
-        for t, n, dt, name in ((out.context_lens, B, torch.int32, "context_lens"),
-                               (out.query_start, B + 1, torch.int32, "query_start"),
-                               (out.slot_mapping, num_tokens, torch.int64, "slot_mapping"),
-                               (out.positions, num_tokens, torch.int32, "positions"),
-                               (out.token_seq, num_tokens, torch.int32, "token_seq"),
-                               (out.pool_head, 1, torch.int32, "pool_head")):
-            _need(t, dt, f"out.{name}")
-            if t.numel() != n:
-                raise ValueError(f"out.{name} must hold {n} values")
-    _check("idx_plan_step", lib.idx_plan_step(
-        cached_lens.data_ptr(), new_lens.data_ptr(), B, block_table.data_ptr(),
-        block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), pool_head.data_ptr(),
-        out.pool_head.data_ptr(), num_blocks, page_size, out.context_lens.data_ptr(),
-        out.query_start.data_ptr(), out.slot_mapping.data_ptr(), out.positions.data_ptr(),
-        out.token_seq.data_ptr(), num_tokens, _ptr(errors), _stream(stream)))
-    return out
+    return StepPlan(*_call(_serving.plan_step, stream, cached_lens, new_lens, block_table,
+                           free_pages, pool_head, num_tokens, num_blocks, page_size, out, errors))
 
 
 def rope_table(num_pos: int, rot_dim: int, base: float = 10000.0, scaling: str | None = None,
                factor: float = 1.0, orig_len: int = 0, beta_fast: float = 32.0,
                beta_slow: float = 1.0, mscale: float | None = None, pos0: int = 0, out=None,
-               device=None, stream=None):
+               stream=None):
     """Rotary tables (cos, sin), each [num_pos, rot_dim/2] fp32, for positions
     pos0 on.  scaling: None, "linear", "ntk" or "yarn" (which needs orig_len,
     the length the frequencies were trained for).  mscale multiplies every
@@ -529,65 +509,18 @@ def rope_table(num_pos: int, rot_dim: int, base: float = 10000.0, scaling: str |
         raise ValueError(f"scaling must be one of {sorted(filter(None, ROPE_SCALINGS))} or None")
     if mscale is None:
         mscale = 0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1.0 else 1.0
-    if out is None:
-        n, half = max(num_pos, 0), max(rot_dim // 2, 0)
-        cos = _empty((n, half), torch.float32, device or "cuda", stream)
-        sin = _empty((n, half), torch.float32, device or "cuda", stream)
-    else:
-        cos, sin = out
-        for t, name in ((cos, "out[0]"), (sin, "out[1]")):
-            _need(t, torch.float32, name)
-            if t.shape != (num_pos, rot_dim // 2):
-                raise ValueError(f"{name} must be [num_pos, rot_dim / 2]")
-    _check("idx_rope_table", lib.idx_rope_table(
-        pos0, num_pos, rot_dim, base, ROPE_SCALINGS[scaling], factor, orig_len, beta_fast,
-        beta_slow, mscale, cos.data_ptr(), sin.data_ptr(), _stream(stream)))
-    return cos, sin
+    cos, sin = (None, None) if out is None else out
+    return _call(_serving.rope_table, stream, num_pos, rot_dim, base, ROPE_SCALINGS[scaling],
+                 factor, orig_len, beta_fast, beta_slow, mscale, pos0, cos, sin)
 
 
 def new_kv_cache(num_blocks: int, heads: int, head_dim: int, dtype=torch.bfloat16,
                  page_size: int = PAGE_SIZE, device=None):
     """A zeroed paged key-value cache: (k, v), each [num_blocks, heads,
     page_size, head_dim] of bf16, fp16 or float8_e4m3fn."""
-    return tuple(torch.zeros((num_blocks, heads, page_size, head_dim), dtype=torch.uint8
-                             if dtype == torch.float8_e4m3fn else dtype,
+    raw = torch.uint8 if dtype == torch.float8_e4m3fn else dtype
+    return tuple(torch.zeros((num_blocks, heads, page_size, head_dim), dtype=raw,
                              device=device or "cuda").view(dtype) for _ in range(2))
-
-
-def _kv_struct(k_cache, v_cache, k_scale, v_scale):
-    if not (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor)):
-        raise TypeError("k_cache and v_cache must be torch.Tensors")
-    dt = DTYPES.get(k_cache.dtype)
-    if dt is None or v_cache.dtype != k_cache.dtype:
-        raise TypeError("k_cache and v_cache must both be bfloat16, float16 or float8_e4m3fn")
-    if not (k_cache.is_cuda and v_cache.is_cuda):
-        raise ValueError("k_cache and v_cache must be CUDA tensors")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must be [num_blocks, heads, page_size, head_dim]")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("k_cache and v_cache must have unit stride in the last dim")
-    nb, heads, page, dim = k_cache.shape
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None:
-            _need(t, torch.float32, name)
-            if t.numel() != heads:
-                raise ValueError(f"{name} must have one entry per kv head")
-    return KvCacheStruct(k_cache.data_ptr(), v_cache.data_ptr(),
-                         None if k_scale is None else k_scale.data_ptr(),
-                         None if v_scale is None else v_scale.data_ptr(), nb, ks[0], ks[1], ks[2],
-                         vs[0], vs[1], vs[2], page, heads, dim, dt)
-
-
-def _heads_of(t, name, n, dim, dtype):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != dim or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [{n}, heads, {dim}] with unit stride in the last dim")
 
 
 def qk_norm_rope_insert(q, k, v, q_weight, k_weight, eps: float, positions, cos, sin,
@@ -600,50 +533,9 @@ def qk_norm_rope_insert(q, k, v, q_weight, k_weight, eps: float, positions, cos,
     may be slices of one projection; caches [num_blocks, Hkv, page_size, D] of
     the same type or float8_e4m3fn (codes hold x / scale).  Returns the turned
     queries [N, Hq, D] (q_out; q itself where it is contiguous is allowed)."""
-    kv = _kv_struct(k_cache, v_cache, k_scale, v_scale)
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    N, dim = q.shape[0], kv.head_dim
-    _heads_of(q, "q", N, dim, q.dtype)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    for t, name in ((k, "k"), (v, "v")):
-        _heads_of(t, name, N, dim, q.dtype)
-        if t.shape[1] != kv.heads:
-            raise ValueError(f"{name} must have the cache's {kv.heads} heads")
-    _need(slot_mapping, torch.int64, "slot_mapping")
-    if slot_mapping.numel() != N:
-        raise ValueError("slot_mapping must have one entry per token")
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, torch.float32, name)
-            if t.numel() != dim:
-                raise ValueError(f"{name} must have head_dim entries")
-    num_pos = 0
-    if rot_dim > 0:
-        _need(positions, torch.int32, "positions")
-        _need(cos, torch.float32, "cos")
-        _need(sin, torch.float32, "sin")
-        if positions.numel() != N:
-            raise ValueError("positions must have one entry per token")
-        if cos.shape != sin.shape or cos.dim() != 2 or cos.shape[1] != rot_dim // 2:
-            raise ValueError("cos/sin must be [num_pos, rot_dim / 2]")
-        num_pos = cos.shape[0]
-    if q_out is None:
-        q_out = _empty(q.shape, q.dtype, q.device, stream)
-    else:
-        _need(q_out, q.dtype, "q_out")
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
-    turn = rot_dim > 0
-    _check("idx_qk_norm_rope_insert", lib.idx_qk_norm_rope_insert(
-        q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1),
-        v.data_ptr(), v.stride(0), v.stride(1), N, q.shape[1], DTYPES[q.dtype], _ptr(q_weight),
-        _ptr(k_weight), eps, _ptr(positions) if turn else None, _ptr(cos) if turn else None,
-        _ptr(sin) if turn else None, num_pos, rot_dim, 1 if interleaved else 0,
-        slot_mapping.data_ptr(), q_out.data_ptr(), ctypes.byref(kv), _ptr(errors),
-        _stream(stream)))
-    return q_out
+    return _call(_serving.qk_norm_rope_insert, stream, q, k, v, q_weight, k_weight, eps,
+                 positions, cos, sin, rot_dim, slot_mapping, k_cache, v_cache, interleaved,
+                 k_scale, v_scale, q_out, errors)
 
 
 def paged_attention_workspace_bytes(B: int, next_n: int, Hq: int, Hkv: int,
@@ -665,45 +557,7 @@ def paged_attention(q, k_cache, v_cache, block_table, context_lens, next_n: int 
     > 0 bounds scores by softcap * tanh(score / softcap).  Returns out
     [B*next_n, Hq, D] of q's type, with return_lse also ln sum exp of the
     scores ([B*next_n, Hq] fp32)."""
-    kv = _kv_struct(k_cache, v_cache, k_scale, v_scale)
-    _need(block_table, torch.int32, "block_table")
-    _need(context_lens, torch.int32, "context_lens")
-    B, dim = context_lens.numel(), kv.head_dim
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError("block_table must be [B, max_blocks]")
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    rows = B * next_n
-    _heads_of(q, "q", rows, dim, q.dtype)
-    Hq, k = q.shape[1], 0
-    if topk is not None:
-        _need(topk, torch.int32, "topk")
-        if topk.dim() != 2 or topk.shape[0] != rows:
-            raise ValueError("topk must be [B * next_n, k]")
-        k = topk.shape[1]
-    if workspace is None:
-        n = paged_attention_workspace_bytes(B, next_n, Hq, kv.heads, dim)
-        workspace = _empty(max(n, 256), torch.uint8, q.device, stream)
-    else:
-        _need(workspace, torch.uint8, "workspace")
-    if out is None:
-        out = _empty((rows, Hq, dim), q.dtype, q.device, stream)
-    else:
-        _need(out, q.dtype, "out")
-        if out.shape != (rows, Hq, dim):
-            raise ValueError("out must be [B * next_n, Hq, D]")
-    if lse is None:
-        if return_lse:
-            lse = _empty((rows, Hq), torch.float32, q.device, stream)
-    else:
-        _need(lse, torch.float32, "lse")
-        if lse.shape != (rows, Hq):
-            raise ValueError("lse must be [B * next_n, Hq]")
-    _check("idx_paged_attention", lib.idx_paged_attention(
-        q.data_ptr(), q.stride(0), q.stride(1), DTYPES[q.dtype], B, next_n, Hq, ctypes.byref(kv),
-        block_table.data_ptr(), block_table.shape[1], context_lens.data_ptr(), _ptr(topk), k,
-        dim ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(), _ptr(lse),
-        workspace.data_ptr(), workspace.numel(), _ptr(errors), _stream(stream)))
-    return (out, lse) if return_lse else out
+    o, l = _call(_serving.paged_attention, stream, q, k_cache, v_cache, block_table, context_lens,
+                 next_n, scale, softcap, window, topk, k_scale, v_scale, workspace, out, lse,
+                 return_lse, errors)
+    return (o, l) if return_lse else o

@@ -1,7 +1,9 @@
-"""Builds libidx.so in-tree from csrc/*.cu with nvcc for sm_103a.
+"""Builds libidx.so in-tree from csrc/*.cu with nvcc for sm_103a, and
+_serving.so, the compiled part of the Python binding, from csrc/serving_py.cpp
+with g++ against PyTorch's headers.
 
 Each translation unit compiles in parallel; the objects go to _build/ and the
-shared library next to this file.  A rebuild is skipped when the library is
+shared libraries next to this file.  A rebuild is skipped when the libraries are
 newer than every source and header.
 """
 from __future__ import annotations
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libidx.so")
+EXT = os.path.join(HERE, "_serving.so")
+EXT_SOURCE = os.path.join(CSRC, "serving_py.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-Xcompiler", "-fvisibility=hidden",
@@ -36,15 +41,15 @@ def _sources():
 
 
 def _deps():
-    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+    return (_sources() + [EXT_SOURCE] + glob.glob(os.path.join(CSRC, "*.cuh")) +
             glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
             [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(EXT)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -64,15 +69,37 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
+    def run(cmd, what):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+    ext_obj = os.path.join(BUILD, "serving_py.o")
+    ext_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               f"-I{INCLUDE}", f"-isystem{torch_dir}/include",
+               f"-isystem{torch_dir}/include/torch/csrc/api/include",
+               f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda_include}",
+               "-c", EXT_SOURCE, "-o", ext_obj]
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        ext = ex.submit(run, ext_cmd, f"g++ on {EXT_SOURCE}")
         objs = list(ex.map(compile_one, srcs))
+        ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = EXT + f".tmp{os.getpid()}"
+    run(["g++", "-shared", "-o", tmp, ext_obj, f"-L{HERE}", "-l:libidx.so", f"-L{torch_dir}/lib",
+         "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+         "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_dir}/lib"], "link of the serving binding")
+    os.replace(tmp, EXT)
     return LIB
 
 
