@@ -137,6 +137,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// A capped score in log2 units: c log2(e) tanh(y) with tanh(y) = 1 - 2 / (1 + e^2y),
+// off by at most 2^-21 c (the exponential's and the reciprocal's 2^-22 each).
+// With the library's tanhf the ragged capped case took 25.0 us instead of 24.0.
+__device__ __forceinline__ float capped(float y, float c_log2e) {
+  return fmaf(-2.f * c_log2e, __fdividef(1.f, 1.f + ex2(2.f * kLog2e * y)), c_log2e);
+}
+
 // Shared-memory offset of 16-byte chunk c of row r: the chunk index is XORed
 // with the row so that eight rows' equal chunks lie in eight bank groups
 // (64-byte rows: two rows per 128 bytes).
@@ -297,7 +304,7 @@ struct KeysOnM {
     for (int kg = 0; kg < KS / 16; ++kg)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        s[kg][e] = softcap * kLog2e * tanhf(s[kg][e] * (e & 1 ? f.y : f.x));
+        s[kg][e] = capped(s[kg][e] * (e & 1 ? f.y : f.x), softcap * kLog2e);
   }
   __device__ __forceinline__ void mask(const Sight& v, int lane) {
     const int g = lane >> 2, c4 = lane & 3;
@@ -504,7 +511,7 @@ struct RowsOnM {
       for (int i = 0; i < KS / 8; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          s[mt][i][e] = softcap * kLog2e * tanhf(s[mt][i][e] * f.f[mt][e >> 1]);
+          s[mt][i][e] = capped(s[mt][i][e] * f.f[mt][e >> 1], softcap * kLog2e);
   }
   __device__ __forceinline__ void mask(const Sight& v, int lane) {
     const int g = lane >> 2, c4 = lane & 3;

@@ -112,6 +112,14 @@ Tensor empty(at::IntArrayRef sizes, ScalarType dtype) {
   return at::detail::empty_cuda(sizes, dtype, c10::Device(c10::kCUDA, c10::cuda::current_device()),
                                 std::nullopt);
 }
+// n values of dtype at element `at` of t's memory.
+Tensor part_of(const Tensor& t, ScalarType dtype, int64_t at, int64_t n) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(),
+                                                   c10::scalarTypeToTypeMeta(dtype));
+  impl->set_storage_offset(at);
+  impl->set_sizes_contiguous({n});
+  return Tensor(std::move(impl));
+}
 idx_stream_t stream() {
   return reinterpret_cast<idx_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
 }
@@ -214,11 +222,21 @@ PyObject* plan_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const char* names[6] = {"out.context_lens", "out.query_start", "out.slot_mapping",
                             "out.positions", "out.token_seq", "out.pool_head"};
     Tensor o[6];
-    for (int i = 0; i < 6; ++i) {
-      const ScalarType t = i == 2 ? ScalarType::Long : ScalarType::Int;
-      if (a[8] == Py_None) {
-        o[i] = empty({sizes[i]}, t);
-      } else {
+    if (a[8] == Py_None) {
+      // one allocation: the slots first, on its 8 bytes, then the 32-bit arrays
+      const Tensor all = empty({2 * tokens + 2 * B + 2 + 2 * tokens}, ScalarType::Int);
+      int64_t at = 2 * tokens;
+      for (int i = 0; i < 6; ++i) {
+        if (i == 2) {
+          o[i] = part_of(all, ScalarType::Long, 0, tokens);
+        } else {
+          o[i] = part_of(all, ScalarType::Int, at, sizes[i]);
+          at += sizes[i];
+        }
+      }
+    } else {
+      for (int i = 0; i < 6; ++i) {
+        const ScalarType t = i == 2 ? ScalarType::Long : ScalarType::Int;
         if (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 6) type_error("out must be a StepPlan");
         o[i] = need(PyTuple_GET_ITEM(a[8], i), t, names[i]);
         if (o[i].numel() != sizes[i])
