@@ -1079,10 +1079,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 template <int D, int CT, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, CT, NT>;
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      paged_attn_kernel<D, CT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-  if (attr != cudaSuccess) return attr;
-  return launch_dependent(paged_attn_kernel<D, CT, NT>, dim3(a.grid), dim3(kThreads), C::kSmem,
+  auto kern = paged_attn_kernel<D, CT, NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(a.grid), dim3(kThreads), C::kSmem,
                           stream, a);
 }
 
