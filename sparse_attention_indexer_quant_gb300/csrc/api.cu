@@ -35,14 +35,17 @@ idx_status ok() {
   return IDX_OK;
 }
 
-// Generations of the fused call's work-item counter: distinct per call (of the
-// process), nonzero (a zero-filled workspace matches no call), below 2^40.
+// Generations of a call's work-item counters: distinct per call (of the
+// process), nonzero (a zero-filled workspace matches no call), below 2^40.  The
+// call's number is spread over the 40 bits by an odd factor (a bijection), so
+// that small numbers or small floats that an uninitialised workspace holds are
+// no call's generation either.
 unsigned long long next_item_generation() {
   static std::atomic<unsigned long long> g_next{1};
   constexpr unsigned long long kMask = (1ull << (64 - idx::kItemBits)) - 1ull;
   unsigned long long g = g_next.fetch_add(1) & kMask;
   while (g == 0) g = g_next.fetch_add(1) & kMask;
-  return g;
+  return (g * 0x9E3779B97Full) & kMask;
 }
 
 }  // namespace idx

@@ -733,7 +733,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         base = req * HR * list_units;
       } else {
         int before = 0;  // units of the requests before this round's
-        for (int b0 = 0;; b0 += kThreads) {
+        if (tid == 0) s_req = -1;
+        for (int b0 = 0; b0 < reqs; b0 += kThreads) {
           const int b = b0 + tid;
           const int mine = b < reqs ? span_of(b).units * HR : 0;
           int incl = warp_incl_sum(mine, lane);
@@ -757,6 +758,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         __syncthreads();
         req = s_req;
         base = s_base;
+        if (req < 0) break;  // the lengths changed during the call
       }
     }
 
