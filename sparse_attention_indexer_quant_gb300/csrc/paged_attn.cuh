@@ -167,6 +167,11 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 // 2^-(K+1), 2^-(K+1), as far as the smallest segments keep kMinSegment units.
 // Segments weigh whole 2^-(K+1) / R parts of the units, the first `rem` parts
 // one unit more than the others.
+//
+// With one level (few units a CTA) segments are first tried along the items:
+// every item in pieces of q units, at most R pieces in all, q from the equal
+// share up to about a quarter more.  A piece lies in one item, so no CTA sets a
+// second one up, which costs about as much as three units.
 constexpr int kMinSegment = 5;
 struct Cut {
   int R, K, U, part, rem;
@@ -207,12 +212,13 @@ struct Span {
 };
 
 // What a tile's masking goes by: key kk of the tile (keys key0 ..) is seen by
-// row r where the table has its place and it lies in [end_r - window, end_r).
+// row r where the table has its place and, of a whole context, where it lies in
+// [end_r - window, end_r).
+template <bool listed>
 struct Sight {
   const uint32_t* tab;  // of the sub-range
   const int* end;       // per row of the item, in shared memory
   int tile0, key0, window;
-  bool listed;
   __device__ __forceinline__ bool there(int kk) const {
     return tab[listed ? tile0 + kk : (tile0 + kk) / 16] != kNone;
   }
@@ -306,7 +312,8 @@ struct KeysOnM {
       for (int e = 0; e < 4; ++e)
         s[kg][e] = capped(s[kg][e] * (e & 1 ? f.y : f.x), softcap * kLog2e);
   }
-  __device__ __forceinline__ void mask(const Sight& v, int lane) {
+  template <bool LISTED>
+  __device__ __forceinline__ void mask(const Sight<LISTED>& v, int lane) {
     const int g = lane >> 2, c4 = lane & 3;
 #pragma unroll
     for (int kg = 0; kg < KS / 16; ++kg)
@@ -513,7 +520,8 @@ struct RowsOnM {
         for (int e = 0; e < 4; ++e)
           s[mt][i][e] = capped(s[mt][i][e] * f.f[mt][e >> 1], softcap * kLog2e);
   }
-  __device__ __forceinline__ void mask(const Sight& v, int lane) {
+  template <bool LISTED>
+  __device__ __forceinline__ void mask(const Sight<LISTED>& v, int lane) {
     const int g = lane >> 2, c4 = lane & 3;
 #pragma unroll
     for (int i = 0; i < KS / 8; ++i)
@@ -655,14 +663,14 @@ struct TileOf<D, CT, 1, KS> {
   using type = KeysOnM<D, CT, KS>;
 };
 
-template <int D, int CT, int NT>
+template <int D, int CT, int NT, bool listed>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, CT, NT>::kOcc))
 paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<D, CT, NT>;
   constexpr bool F8 = C::kF8, MB = C::kMmaBf16;
   constexpr int KS = C::kKS, ROWB = C::kRowB, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_warp[kWarps];
+  __shared__ int s_warp[kWarps], s_pieces[kWarps][4];
   __shared__ int s_base, s_req, s_seg;
   // log2 score per product (with a cap: its argument), and ones for capped scores
   __shared__ __align__(8) float s_mult[C::kRows], s_one[C::kRows];
@@ -678,7 +686,6 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   uint32_t* vtab = a.one_table ? tab : tab + kTab / 2;
   const int tab_words = a.one_table ? kTab : kTab / 2;
 
-  const bool listed = a.topk_idx != nullptr;
   const int Hkv = a.kv.heads, HR = Hkv * a.row_tiles;
   const int page_mask = (1 << a.page_shift) - 1;
   const long long cap = (long long)a.max_blocks << a.page_shift;
@@ -712,11 +719,44 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
     }
   }
   const Cut cut(a.split ? U : (int)gridDim.x, (int)gridDim.x);
+  int q = 0, segments = cut.segments();  // q > 0: units of a piece
+  if (a.split && cut.K == 0) {
+    const int q0 = (U + (int)gridDim.x - 1) / (int)gridDim.x, step = max(1, q0 / 12);
+    int pieces[4] = {0, 0, 0, 0};
+    if (listed) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pieces[j] = reqs * ((list_units + q0 + j * step - 1) / (q0 + j * step));
+    } else {
+      for (int b = tid; b < reqs; b += kThreads) {
+        const int units = span_of(b).units;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pieces[j] += (units + q0 + j * step - 1) / (q0 + j * step);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        pieces[j] = __reduce_add_sync(~0u, pieces[j]);
+        if (lane == 0) s_pieces[warp][j] = pieces[j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        pieces[j] = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) pieces[j] += s_pieces[w][j];
+      }
+    }
+#pragma unroll
+    for (int j = 3; j >= 0; --j)
+      if (pieces[j] <= (int)gridDim.x / HR) {
+        q = q0 + j * step;
+        segments = pieces[j] * HR;
+      }
+  }
   // every CTA is running: the join may take the room of those that finish first
   pdl_launch_dependents();
   const bool use_cap = a.softcap > 0.f;
 
-  for (int seg = blockIdx.x; seg < cut.segments();) {
+  for (int seg = blockIdx.x; seg < segments;) {
     // ---- the segment's units [u0, u1), and the request its first unit belongs to
     int u0, u1, base, req;  // base: first unit of request `req`
     if (!a.split) {  // one CTA per item; units are counted from its request's first
@@ -726,17 +766,18 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       u0 = (seg % HR) * units;
       u1 = u0 + units;
     } else {
-      u0 = cut.start(seg);
-      u1 = cut.start(seg + 1);
+      // requests weigh their units or pieces; the one that holds unit or piece x
+      const int x = q > 0 ? seg : cut.start(seg);
+      auto weight = [&](int units) -> int { return (q > 0 ? (units + q - 1) / q : units) * HR; };
       if (listed) {
-        req = u0 / (HR * list_units);
-        base = req * HR * list_units;
+        req = x / weight(list_units);
+        base = req * weight(list_units);
       } else {
-        int before = 0;  // units of the requests before this round's
+        int before = 0;  // weights of the requests before this round's
         if (tid == 0) s_req = -1;
         for (int b0 = 0; b0 < reqs; b0 += kThreads) {
           const int b = b0 + tid;
-          const int mine = b < reqs ? span_of(b).units * HR : 0;
+          const int mine = b < reqs ? weight(span_of(b).units) : 0;
           int incl = warp_incl_sum(mine, lane);
           __syncthreads();
           if (lane == 31) s_warp[warp] = incl;
@@ -748,17 +789,26 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             total += s_warp[w];
           }
           const int first = before + incl - mine;
-          if (mine > 0 && first <= u0 && u0 < first + mine) {
+          if (mine > 0 && first <= x && x < first + mine) {
             s_req = b;
             s_base = first;
           }
           before += total;
-          if (before > u0) break;
+          if (before > x) break;
         }
         __syncthreads();
         req = s_req;
         base = s_base;
         if (req < 0) break;  // the lengths changed during the call
+      }
+      u0 = x;
+      u1 = q > 0 ? x + 1 : cut.start(seg + 1);
+      if (q > 0) {  // the piece's units, counted from its request's first
+        const int units = listed ? list_units : span_of(req).units, per = (units + q - 1) / q;
+        const int hr = (x - base) / per, piece = x - base - hr * per;
+        base = 0;
+        u0 = hr * units + piece * q;
+        u1 = hr * units + min(units, (piece + 1) * q);
       }
     }
 
@@ -969,7 +1019,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           cp_async_commit();
           put = put + 1 == NS ? 0 : put + 1;
         };
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < NS; ++i) issue(i);
 
         tile.load_q(q_u, lane);
@@ -996,7 +1046,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
                     (a.window == 0 || key0 >= end0 + n_tok - 1 - a.window);
           }
           if (use_cap) tile.cap(a.softcap, s_mult, lane);
-          if (!whole) tile.mask(Sight{tab, s_end, tile0, key0, a.window, listed}, lane);
+          if (!whole) tile.mask(Sight<listed>{tab, s_end, tile0, key0, a.window}, lane);
 
           cp_async_wait_group<NS - 1>();
           __syncwarp();
@@ -1023,7 +1073,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       // first segment's last (or only) part, then the following segments' first parts
       const int part = 2 * seg + (u == u0 ? 0 : 1);
       if (a.split && ta == 0 && tid == 0)
-        a.desc[req * HR + hr] = make_int2(part, cut.owner(u + units - 1) - seg + 1);
+        a.desc[req * HR + hr] =
+            make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(u + units - 1) - seg + 1);
       constexpr int QPR = D / 4;  // float4 quads per row
       for (int i = tid; i < rows * QPR; i += kThreads) {
         const int r = i / QPR, d = (i % QPR) * 4;
@@ -1081,7 +1132,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 template <int D, int CT, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, CT, NT>;
-  auto kern = paged_attn_kernel<D, CT, NT>;
+  auto kern = a.topk_idx ? paged_attn_kernel<D, CT, NT, true> : paged_attn_kernel<D, CT, NT, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3(a.grid), dim3(kThreads), C::kSmem,
