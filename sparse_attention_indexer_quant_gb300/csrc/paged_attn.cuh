@@ -162,7 +162,12 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
   return x;
 }
 
-// The cut of U units into segments by R CTAs.  One level of A = min(R, U)
+// An item costs its units and about as much time again as kSetup of them: query
+// rows, table, first loads, the sums of eight warps.  Cuts weigh it so, the
+// setup first.
+constexpr int kSetup = 3;
+
+// The cut of U units (setups counted) into segments by R CTAs.  One level of A = min(R, U)
 // equal segments, or K + 1 levels of R: 3/4 of the units, then 1/8, 1/16, ...,
 // 2^-(K+1), 2^-(K+1), as far as the smallest segments keep kMinSegment units.
 // Segments weigh whole 2^-(K+1) / R parts of the units, the first `rem` parts
@@ -171,7 +176,7 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 // With one level (few units a CTA) segments are first tried along the items:
 // every item in pieces of q units, at most R pieces in all, q from the equal
 // share up to about a quarter more.  A piece lies in one item, so no CTA sets a
-// second one up, which costs about as much as three units.
+// second one up.
 constexpr int kMinSegment = 5;
 struct Cut {
   int R, K, U, part, rem;
@@ -706,10 +711,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   int U = 0;  // below 2^31, as the caller has checked
   if (a.split) {
     if (listed) {
-      U = reqs * HR * list_units;
+      U = reqs * HR * (list_units + kSetup);
     } else {
       int sum = 0;
-      for (int b = tid; b < reqs; b += kThreads) sum += span_of(b).units;
+      for (int b = tid; b < reqs; b += kThreads) sum += span_of(b).units + kSetup;
       sum = warp_incl_sum(sum, lane);
       if (lane == 31) s_warp[warp] = sum;
       __syncthreads();
@@ -721,7 +726,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   const Cut cut(a.split ? U : (int)gridDim.x, (int)gridDim.x);
   int q = 0, segments = cut.segments();  // q > 0: units of a piece
   if (a.split && cut.K == 0) {
-    const int q0 = (U + (int)gridDim.x - 1) / (int)gridDim.x, step = max(1, q0 / 12);
+    const int real = U - reqs * HR * kSetup;
+    const int q0 = (real + (int)gridDim.x - 1) / (int)gridDim.x, step = max(1, q0 / 12);
     int pieces[4] = {0, 0, 0, 0};
     if (listed) {
 #pragma unroll
@@ -756,6 +762,15 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   pdl_launch_dependents();
   const bool use_cap = a.softcap > 0.f;
 
+  // units of setup that count in this call's segments
+  const int setup = a.split && q == 0 ? kSetup : 0;
+  // thread 0 fetches the CTA's next segment
+  auto claim = [&]() {
+    if (a.split && cut.K > 0 && tid == 0) {
+      const uint32_t t = claim_item(a.counter, a.gen, a.errors);
+      s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
+    }
+  };
   for (int seg = blockIdx.x; seg < segments;) {
     // ---- the segment's units [u0, u1), and the request its first unit belongs to
     int u0, u1, base, req;  // base: first unit of request `req`
@@ -768,7 +783,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
     } else {
       // requests weigh their units or pieces; the one that holds unit or piece x
       const int x = q > 0 ? seg : cut.start(seg);
-      auto weight = [&](int units) -> int { return (q > 0 ? (units + q - 1) / q : units) * HR; };
+      auto weight = [&](int units) -> int { return (q > 0 ? (units + q - 1) / q : units + setup) * HR; };
       if (listed) {
         req = x / weight(list_units);
         base = req * weight(list_units);
@@ -812,17 +827,29 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       }
     }
 
+    bool claimed = false;
     for (int u = u0; u < u1;) {
       // ---- the item at unit u, and the part of it that is this segment's
+      int req_next = req;
       const int b = listed ? req / a.next_n : req;
       const int tok0 = listed ? req : req * a.next_n;  // query row of the item's first row
       const int n_tok = listed ? 1 : a.next_n;
       const Span sp = span_of(b);
       const int units = listed ? list_units : sp.units;
-      const int hr = (u - base) / units;
+      const int cost = setup + units, hr = (u - base) / cost;
+      const int off = u - base - hr * cost, stop = min(cost, off + (u1 - u));
       const int h = hr / a.row_tiles, rt = hr % a.row_tiles;
-      const int ta = u - base - hr * units;
-      const int tb = min(units, ta + (u1 - u));
+      const int ta = max(0, off - setup), tb = max(0, stop - setup);
+      const bool first_item = u == u0;
+      u += stop - off;
+      if (u - base >= cost * HR) {
+        base += cost * HR;
+        ++req_next;
+      }
+      if (ta == tb) {  // the segment ends in the item's setup
+        req = req_next;
+        continue;
+      }
       const int row0 = rt * C::kRows;
       const int rows = min(C::kRows, a.rows - row0);
       constexpr int EB = F8 ? 1 : 2;  // bytes of a cached value
@@ -1061,20 +1088,19 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 
       // ---- the warps' sums become one: each leaves its own in its ring
       tile.leave(reinterpret_cast<float*>(ring), C::kPitch, s_ml[warp], rows, lane);
-      const bool last_item = u + (tb - ta) >= u1;
-      if (last_item && a.split && cut.K > 0 && tid == 0) {
-        // the next segment, claimed while the sums are joined
-        const uint32_t t = claim_item(a.counter, a.gen, a.errors);
-        s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
+      if (u + setup >= u1) {  // nothing more in this segment
+        claimed = true;
+        claim();  // while the sums are joined
       }
       __syncthreads();
       const bool complete = ta == 0 && tb == units;
       // partial 2 s is a segment's first part, 2 s + 1 its last; an item's parts are its
       // first segment's last (or only) part, then the following segments' first parts
-      const int part = 2 * seg + (u == u0 ? 0 : 1);
+      const int item_end = u + cost - stop;  // in the cut's units
+      const int part = 2 * seg + (first_item ? 0 : 1);
       if (a.split && ta == 0 && tid == 0)
         a.desc[req * HR + hr] =
-            make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(u + units - 1) - seg + 1);
+            make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(item_end - 1) - seg + 1);
       constexpr int QPR = D / 4;  // float4 quads per row
       for (int i = tid; i < rows * QPR; i += kThreads) {
         const int r = i / QPR, d = (i % QPR) * 4;
@@ -1118,14 +1144,15 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       }
       __syncthreads();  // the rings, the table and the query rows are refilled next
 
-      u += tb - ta;
-      if (u - base >= units * HR) {
-        base += units * HR;
-        ++req;
-      }
+      req = req_next;
     }
     if (!a.split || cut.K == 0) break;
+    if (!claimed) {
+      claim();
+      __syncthreads();
+    }
     seg = s_seg;
+    __syncthreads();  // read by all before the next claim
   }
 }
 

@@ -424,7 +424,7 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
   a.split = units > 2;
   const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
-  if (units * items > INT32_MAX || items * a.part_rows > INT32_MAX)
+  if ((units + 64) * items > INT32_MAX || items * a.part_rows > INT32_MAX)
     return fail(IDX_ERR_INVALID_ARG, "%lld query row tiles of up to %lld keys: too much for one call",
                 (long long)items, (long long)keys);
   a.grid = (int32_t)grid;
