@@ -764,9 +764,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 
   // units of setup that count in this call's segments
   const int setup = a.split && q == 0 ? kSetup : 0;
-  // thread 0 fetches the CTA's next segment
+  // The last thread, which has the least to do when sums are joined, fetches the
+  // CTA's next segment.
   auto claim = [&]() {
-    if (a.split && cut.K > 0 && tid == 0) {
+    if (a.split && cut.K > 0 && tid == kThreads - 1) {
       const uint32_t t = claim_item(a.counter, a.gen, a.errors);
       s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
     }
@@ -965,12 +966,14 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
               for (int d = LQ / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, d));
               // largest magnitude to [2^14, 2^15): all products with codes stay finite
+              // (tiny rows: times 2^126; rows with an infinity or NaN: as they are)
               int e = 0;
-              if (a.q_bf16 && amax > 0.f && amax < INFINITY) e = 14 - ilogbf(amax);
+              if (a.q_bf16 && amax < INFINITY) e = min(126, 141 - (int)(__float_as_uint(amax) >> 23));
+              const float up = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = pack2<false>(ldexpf(x[2 * j], e), ldexpf(x[2 * j + 1], e));
-              mult = ldexpf(mult * (a.kv.k_scale ? __ldg(a.kv.k_scale + h) : 1.f), -e);
+              for (int j = 0; j < 4; ++j) w[j] = pack2<false>(x[2 * j] * up, x[2 * j + 1] * up);
+              mult *= (a.kv.k_scale ? __ldg(a.kv.k_scale + h) : 1.f) *
+                      __uint_as_float((uint32_t)(127 - e) << 23);
             }
             if (QP * kThreads == C::kRows * LQ || r < C::kRows) {
               if (part == 0) {
@@ -1098,7 +1101,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       // first segment's last (or only) part, then the following segments' first parts
       const int item_end = u + cost - stop;  // in the cut's units
       const int part = 2 * seg + (first_item ? 0 : 1);
-      if (a.split && ta == 0 && tid == 0)
+      if (a.split && ta == 0 && tid == kThreads - 1)
         a.desc[req * HR + hr] =
             make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(item_end - 1) - seg + 1);
       constexpr int QPR = D / 4;  // float4 quads per row
