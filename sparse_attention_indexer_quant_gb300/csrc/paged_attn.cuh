@@ -2,17 +2,19 @@
 //
 // Work.  An item is one kv head of one request with its query rows (next_n
 // tokens times the heads of the group; with a selection, one token's group),
-// up to 8 * NT of them.  Its keys are cut into units of 8 * KS, numbered item
-// by item over the whole batch, and the units into segments.  With R resident
-// CTAs the first R segments take three quarters of the units, one segment per
-// CTA; the rest are cut into levels of R segments of 1/8, 1/16, ... that the
-// CTAs claim from a counter as they finish.  (Equal shares alone left the
-// fastest CTA idle for a quarter of the time: CTAs stream at rates up to 30 %
-// apart.)  Which units form a segment depends on the lengths alone, so
-// results do not depend on the order in which CTAs run.  A segment that holds
-// an item whole writes its result; an item that spans segments leaves one
-// partial (running maximum, weight, weighted sum) per segment in the workspace
-// and a second, dependent launch joins them in the order of their keys.
+// up to 8 * NT of them.  Its keys are cut into units of 8 * KS (64 KB of cache
+// for most shapes), numbered item by item over the whole batch, and the units
+// into segments (see Cut).  With R resident CTAs the first R segments take
+// three quarters of the units, one segment per CTA; the rest are cut into
+// levels of R segments of 1/8, 1/16, ... that the CTAs claim from a counter as
+// they finish: with equal shares alone the first CTA was done after 614 us and
+// the last after 817 (64 requests of 8K - 32K keys), as CTAs stream at
+// different rates; 817 became 705.  Which units form a segment depends on the
+// lengths alone, so results do not depend on the order in which CTAs run.  A
+// segment that holds an item whole writes its result; an item that spans
+// segments leaves one partial (running maximum, weight, weighted sum) per
+// segment in the workspace and a second, dependent launch joins them in the
+// order of their keys.
 //
 // Arithmetic.  o = sum_s p_s v_s / sum_s p_s with p_s = 2^(x_s - m), one pass
 // with a running reference m per row that is raised (and the sums rescaled)
@@ -22,11 +24,10 @@
 // dimensions) on M, query rows on N, so that eight rows fill a tile: S^T =
 // K Q^T, then O^T = V^T P^T, P passing from one product's result layout to the
 // other's operand layout by a register transpose (movmatrix).  More rows: query
-// rows on M.  p goes
-// into the second product as two 16-bit terms, hi = round(p) and lo =
-// round(p - hi): one term's rounding (2^-9 in bf16) would be as large as the
-// rounding of the output itself.  8-bit codes are exact in fp16; queries are
-// then brought to fp16 by a power of two per row, which loses nothing of a
+// rows on M.  p goes into the second product as two 16-bit terms, hi = round(p)
+// and lo = round(p - hi): one term's rounding (2^-9 in bf16) would be as large
+// as the rounding of the output itself.  8-bit codes are exact in fp16; queries
+// are then brought to fp16 by a power of two per row, which loses nothing of a
 // bf16 value within 2^-29 of the row's largest.
 //
 // Memory.  2 G flops per byte of cache (G query heads per kv head) is far
@@ -36,6 +37,13 @@
 // ldmatrix); no barrier stands between warps until the item ends.  Rows that
 // no query sees are zero-filled, never read, so whatever a page holds past the
 // context (NaN included) cannot reach a sum.
+//
+// Measured (one call, new inputs in turn): 64 requests of 8K - 32K keys, 32/8
+// heads of 128, bf16, 5.2 GB: 724 us, 7.19 TB/s; 64 x 2048 selected positions
+// (0.54 GB) 94 us, 5.7 TB/s, of which about 10 us are the start of the stream
+// and the join and 8 the spread of the CTAs' ends.  The tensor pipe is 13 - 15 %
+// busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
+// from 32 rows over an E4M3 cache on (0.53 of the copy rate).
 #pragma once
 
 #include <float.h>
