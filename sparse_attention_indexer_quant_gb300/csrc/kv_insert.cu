@@ -213,9 +213,11 @@ cudaError_t launch_d(const KvInsertArgs& a, int sms, cudaStream_t stream) {
   // Four heads a group once they fill every SM's eight blocks, else one.  4000
   // tokens of 32 + 2 x 8 heads of 128: 18.4 us by fours, 28.4 by ones; 1000
   // tokens 6.2 and 7.8; 200 tokens 5.7 and 5.5 (few blocks, one long chain each).
+  // Where fours would be half empty, ones: 20000 tokens of 2 + 2 x 2 heads 17.5
+  // us, by fours 19.4; of 5 + 2 x 2 heads 16.7 and 15.4.
   const int q4 = (a.Hq + 3) / 4, k4 = (a.kv.heads + 3) / 4;
   const int64_t n4 = a.N * (q4 + 2 * k4);
-  if (n4 >= (int64_t)sms * 8 * kGroups)
+  if (n4 >= (int64_t)sms * 8 * kGroups && 2 * (q4 + 2 * k4) < a.Hq + 2 * a.kv.heads)
     return launch_dependent(kv_insert_kernel<D, BF16, CACHE8, PAIRS, 4>,
                             dim3((unsigned)((n4 + kGroups - 1) / kGroups)), dim3(kThreads), 0, stream,
                             a, q4, k4);

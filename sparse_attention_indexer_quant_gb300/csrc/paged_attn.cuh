@@ -683,7 +683,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   constexpr bool F8 = C::kF8, MB = C::kMmaBf16;
   constexpr int KS = C::kKS, ROWB = C::kRowB, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_warp[kWarps], s_pieces[kWarps][4];
+  __shared__ int s_warp[kWarps], s_pieces[kWarps][4], s_last[kWarps];
   __shared__ int s_base, s_req, s_seg;
   // log2 score per product (with a cap: its argument), and ones for capped scores
   __shared__ __align__(8) float s_mult[C::kRows], s_one[C::kRows];
@@ -903,11 +903,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       // units whose page groups of 16 keys (or listed positions) fit the table
       const int sub = tab_words / (listed ? C::kUnit : C::kUnit / 16);
       for (int sa = ta; sa < tb; sa += sub) {
-        const int sb = min(tb, sa + sub);
+        int sb = min(tb, sa + sub);
         if (sa > ta) __syncthreads();  // the previous range's table is done with
         // four entries at a time, their loads issued together (a list entry and
         // then its page id are two dependent round trips)
         constexpr int TB = 4;
+        int last = -1;  // last position found in this thread's entries
         if (listed) {
           const int* list = a.topk_idx + (int64_t)req * a.topk;
           const int my_end = max(0, sp.len - a.next_n + 1 + req % a.next_n);
@@ -928,6 +929,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
               if (i >= n) break;
               const bool ok = id[j] >= 0 && id[j] < a.kv.num_blocks;
               if (!ok && p[j] >= 0 && hr == 0) count_bad_input(a.errors);
+              if (ok) last = i;
               tab[i] = ok ? k_off(id[j], p[j] & page_mask) : kNone;
               if (!a.one_table) vtab[i] = ok ? v_off(id[j], p[j] & page_mask) : kNone;
             }
@@ -1003,7 +1005,18 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             }
           }
         }
+        if (listed) {
+          // units past the last listed position (a short row's list ends in -1) are
+          // not streamed at all
+          last = __reduce_max_sync(~0u, last);
+          if (lane == 0) s_last[warp] = last;
+        }
         __syncthreads();
+        if (listed) {
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) last = max(last, s_last[w]);
+          sb = min(sb, sa + last / C::kUnit + (last < 0 ? 0 : 1));
+        }
 
         // ---- the warp's stream: half stage 2 t is unit sa + t's keys, 2 t + 1 its values
         const int halves = 2 * (sb - sa);
