@@ -2,8 +2,9 @@
 //
 // Work.  An item is one kv head of one request with its query rows (next_n
 // tokens times the heads of the group; with a selection, one token's group),
-// up to 8 * NT of them.  Its keys are cut into units of 8 * KS (64 KB of cache
-// for most shapes), numbered item by item over the whole batch, and the units
+// up to 8 * NT of them.  Many short items are taken by a warp each; else a CTA
+// of eight warps shares an item.  Its keys are cut into units of 8 * KS (64 KB
+// of cache for most shapes), numbered item by item over the whole batch, and the units
 // into segments (see Cut).  With R resident CTAs the first R segments take
 // three quarters of the units, one segment per CTA; the rest are cut into
 // levels of R segments of 1/8, 1/16, ... that the CTAs claim from a counter as
@@ -68,26 +69,36 @@ constexpr float kSlack = 8.f;  // log2 of how far a score may pass the reference
 template <int D, int CT>
 constexpr int row_bytes() { return D * (CT == IDX_E4M3 ? 1 : 2); }
 
-template <int D, int CT, int NT>
+// W warps share an item: the CTA's eight, or one (short items, eight a CTA).
+template <int D, int CT, int NT, int W>
 struct Cfg {
+  static_assert(W == kWarps || W == 1, "");
   static constexpr bool kF8 = CT == IDX_E4M3;
   static constexpr bool kMmaBf16 = CT == IDX_BF16;
   static constexpr int kRowB = row_bytes<D, CT>();
   // keys per warp and unit: 4 KB half stages where rows are short and the sums
   // leave room for 32 keys' scores
-  static constexpr int kKS = attn_keys_per_tile(D, CT, NT);
-  static constexpr int kUnit = kWarps * kKS;
+  static constexpr int kKS = attn_keys_per_tile(D, CT, NT, W);
+  static constexpr int kUnit = W * kKS;
   static constexpr int kRows = 8 * NT;
   static constexpr int kHalf = kRowB * kKS;  // bytes of a half stage
   // two CTAs per SM where 128 registers a thread hold the accumulators
   static constexpr int kOcc = attn_occupancy(D, CT, NT);
-  static constexpr int kStages = (kOcc == 2 ? 12288 : 24576) / kHalf;
+  static constexpr int kPitch = W == 1 ? D : D + 4;  // floats of a row of the merge buffer
+  static constexpr int kSums = kRows * kPitch * 4;
+  // a warp's ring: all the room there is, or with an item per warp two half
+  // stages, 8 KB or the sums
+  static constexpr int kMinRing = kSums > 8192 ? (kSums > 2 * kHalf ? kSums : 2 * kHalf)
+                                               : (2 * kHalf > 8192 ? 2 * kHalf : 8192);
+  static constexpr int kStages = W == 1 ? kMinRing / kHalf : (kOcc == 2 ? 12288 : 24576) / kHalf;
   static constexpr int kRing = kStages * kHalf;
-  static constexpr int kPitch = D + 4;  // floats of a row of the merge buffer
+  static constexpr int kTeams = kWarps / W;
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kSmem = kWarps * kRing + kQBytes + kTab * 4;
-  static_assert(kRows * kPitch * 4 <= kRing, "a warp's sums fit its ring");
-  static_assert(kStages >= 3, "");
+  static constexpr int kTabWords = kTab / kTeams;
+  static constexpr int kSmem = kWarps * kRing + kTeams * (kQBytes + kTabWords * 4);
+  static_assert(kSums <= kRing, "a warp's sums fit its ring");
+  static_assert(kStages >= 2 && kRing % kHalf == 0, "");
+  static_assert(kSmem * kOcc <= 222 * 1024, "");
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
@@ -676,28 +687,37 @@ struct TileOf<D, CT, 1, KS> {
   using type = KeysOnM<D, CT, KS>;
 };
 
-template <int D, int CT, int NT, bool listed>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, CT, NT>::kOcc))
+template <int D, int CT, int NT, bool listed, int W>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, CT, NT, W>::kOcc))
 paged_attn_kernel(const __grid_constant__ AttnArgs a) {
-  using C = Cfg<D, CT, NT>;
+  using C = Cfg<D, CT, NT, W>;
   constexpr bool F8 = C::kF8, MB = C::kMmaBf16;
   constexpr int KS = C::kKS, ROWB = C::kRowB, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_warp[kWarps], s_pieces[kWarps][4], s_last[kWarps];
   __shared__ int s_base, s_req, s_seg;
   // log2 score per product (with a cap: its argument), and ones for capped scores
-  __shared__ __align__(8) float s_mult[C::kRows], s_one[C::kRows];
-  __shared__ int s_end[C::kRows];  // first key past a row's sight
+  __shared__ __align__(8) float s_mults[C::kTeams][C::kRows], s_one[C::kRows];
+  __shared__ int s_ends[C::kTeams][C::kRows];  // first key past a row's sight
   __shared__ float2 s_ml[kWarps][C::kRows];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // the team that shares an item, and this thread's place in it
+  constexpr int TT = 32 * W;
+  const int team = W == 1 ? warp : 0, tw = W == 1 ? 0 : warp, tid = W == 1 ? lane : (int)threadIdx.x;
+  auto sync = [&]() {
+    if (W == 1) __syncwarp(); else __syncthreads();
+  };
+  float* s_mult = s_mults[team];
+  int* s_end = s_ends[team];
   uint8_t* ring = smem + warp * C::kRing;
   const uint32_t ring_u = smem_u32(ring);
-  uint8_t* q_sm = smem + kWarps * C::kRing;
+  uint8_t* q_sm = smem + kWarps * C::kRing + team * C::kQBytes;
   const uint32_t q_u = smem_u32(q_sm);
-  uint32_t* tab = reinterpret_cast<uint32_t*>(q_sm + C::kQBytes);
+  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + kWarps * C::kRing + C::kTeams * C::kQBytes) +
+                  team * C::kTabWords;
   // offsets into k and v: one table where both have the same strides
-  uint32_t* vtab = a.one_table ? tab : tab + kTab / 2;
-  const int tab_words = a.one_table ? kTab : kTab / 2;
+  uint32_t* vtab = a.one_table ? tab : tab + C::kTabWords / 2;
+  const int tab_words = a.one_table ? C::kTabWords : C::kTabWords / 2;
 
   const int Hkv = a.kv.heads, HR = Hkv * a.row_tiles;
   const int page_mask = (1 << a.page_shift) - 1;
@@ -717,7 +737,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   const int reqs = listed ? a.B * a.next_n : a.B;
   const int list_units = (a.topk + C::kUnit - 1) / C::kUnit;
   int U = 0;  // below 2^31, as the caller has checked
-  if (a.split) {
+  const bool split = W == kWarps && a.split;
+  if (split) {
     if (listed) {
       U = reqs * HR * (list_units + kSetup);
     } else {
@@ -731,9 +752,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       U *= HR;
     }
   }
-  const Cut cut(a.split ? U : (int)gridDim.x, (int)gridDim.x);
-  int q = 0, segments = cut.segments();  // q > 0: units of a piece
-  if (a.split && cut.K == 0) {
+  const Cut cut(split ? U : (int)gridDim.x, (int)gridDim.x);
+  // q > 0: units of a piece
+  int q = 0, segments = W == 1 ? reqs * HR : cut.segments();
+  if (split && cut.K == 0) {
     const int real = U - reqs * HR * kSetup;
     const int q0 = (real + (int)gridDim.x - 1) / (int)gridDim.x, step = max(1, q0 / 12);
     int pieces[4] = {0, 0, 0, 0};
@@ -771,19 +793,19 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   const bool use_cap = a.softcap > 0.f;
 
   // units of setup that count in this call's segments
-  const int setup = a.split && q == 0 ? kSetup : 0;
+  const int setup = split && q == 0 ? kSetup : 0;
   // The last thread, which has the least to do when sums are joined, fetches the
   // CTA's next segment.
   auto claim = [&]() {
-    if (a.split && cut.K > 0 && tid == kThreads - 1) {
+    if (split && cut.K > 0 && tid == kThreads - 1) {
       const uint32_t t = claim_item(a.counter, a.gen, a.errors);
       s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
     }
   };
-  for (int seg = blockIdx.x; seg < segments;) {
+  for (int seg = W == 1 ? blockIdx.x * kWarps + warp : blockIdx.x; seg < segments;) {
     // ---- the segment's units [u0, u1), and the request its first unit belongs to
     int u0, u1, base, req;  // base: first unit of request `req`
-    if (!a.split) {  // one CTA per item; units are counted from its request's first
+    if (!split) {  // one team per item; units are counted from its request's first
       const int units = listed ? list_units : span_of(seg / HR).units;
       req = seg / HR;
       base = 0;
@@ -881,20 +903,21 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         if (L < 0 || L > cap) count_bad_input(a.errors);
       }
 
-      // ---- the item's query rows, on their way while the table is made
+      // ---- the item's query rows; a CTA's are on their way while the table is made
       constexpr int LQ = D / 8;  // lanes per row, 16 bytes each
-      constexpr int QP = (C::kRows * LQ + kThreads - 1) / kThreads;
-      uint4 qraw[QP];
+      constexpr int QP = (C::kRows * LQ + TT - 1) / TT;
+      auto q_chunk = [&](int i) -> uint4 {
+        const int r = (i * TT + tid) / LQ, rr = row0 + r;
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) +
+                              (int64_t)(tok0 + rr / a.group) * a.q_ts +
+                              (int64_t)(h * a.group + rr % a.group) * a.q_hs;
+        return __ldg(reinterpret_cast<const uint4*>(src) + tid % LQ);
+      };
+      uint4 qraw[W == 1 ? 1 : QP];
+      if (W > 1) {
 #pragma unroll
-      for (int i = 0; i < QP; ++i) {
-        const int r = (i * kThreads + tid) / LQ, rr = row0 + r;
-        qraw[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const uint16_t* src = static_cast<const uint16_t*>(a.q) +
-                                (int64_t)(tok0 + rr / a.group) * a.q_ts +
-                                (int64_t)(h * a.group + rr % a.group) * a.q_hs;
-          qraw[i] = __ldg(reinterpret_cast<const uint4*>(src) + tid % LQ);
-        }
+        for (int i = 0; i < QP; ++i) qraw[W == 1 ? 0 : i] = q_chunk(i);
       }
 
       typename TileOf<D, CT, NT, KS>::type tile;
@@ -904,7 +927,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       const int sub = tab_words / (listed ? C::kUnit : C::kUnit / 16);
       for (int sa = ta; sa < tb; sa += sub) {
         int sb = min(tb, sa + sub);
-        if (sa > ta) __syncthreads();  // the previous range's table is done with
+        if (sa > ta) sync();  // the previous range's table is done with
         // four entries at a time, their loads issued together (a list entry and
         // then its page id are two dependent round trips)
         constexpr int TB = 4;
@@ -913,11 +936,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           const int* list = a.topk_idx + (int64_t)req * a.topk;
           const int my_end = max(0, sp.len - a.next_n + 1 + req % a.next_n);
           const int n = (sb - sa) * C::kUnit;
-          for (int i0 = tid; i0 < n; i0 += TB * kThreads) {
+          for (int i0 = tid; i0 < n; i0 += TB * TT) {
             int p[TB], id[TB];
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
-              const int i = i0 + j * kThreads, at = sa * C::kUnit + i;
+              const int i = i0 + j * TT, at = sa * C::kUnit + i;
               p[j] = i < n && at < a.topk ? __ldg(list + at) : -1;
             }
 #pragma unroll
@@ -925,7 +948,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
               id[j] = p[j] >= 0 && p[j] < my_end ? __ldg(bt + (p[j] >> a.page_shift)) : -1;
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
-              const int i = i0 + j * kThreads;
+              const int i = i0 + j * TT;
               if (i >= n) break;
               const bool ok = id[j] >= 0 && id[j] < a.kv.num_blocks;
               if (!ok && p[j] >= 0 && hr == 0) count_bad_input(a.errors);
@@ -936,16 +959,16 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           }
         } else {
           const int g0 = (sp.t0 + sa) * (C::kUnit / 16), n = (sb - sa) * (C::kUnit / 16);
-          for (int i0 = tid; i0 < n; i0 += TB * kThreads) {
+          for (int i0 = tid; i0 < n; i0 += TB * TT) {
             int id[TB];
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
-              const int i = i0 + j * kThreads, key = (g0 + i) * 16;
+              const int i = i0 + j * TT, key = (g0 + i) * 16;
               id[j] = i < n && key < sp.len && key + 16 > lo_all ? __ldg(bt + (key >> a.page_shift)) : -1;
             }
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
-              const int i = i0 + j * kThreads, key = (g0 + i) * 16;
+              const int i = i0 + j * TT, key = (g0 + i) * 16;
               if (i >= n) break;
               const bool ok = id[j] >= 0 && id[j] < a.kv.num_blocks;
               // counted once per page, by its first group that is in sight
@@ -959,11 +982,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         }
         if (sa == ta) {
           // ---- query rows to shared memory
-#pragma unroll
+#pragma unroll(W == 1 ? 2 : QP)
           for (int i = 0; i < QP; ++i) {
-            const int r = (i * kThreads + tid) / LQ, part = tid % LQ;
+            const int r = (i * TT + tid) / LQ, part = tid % LQ;
             float mult = fabsf(a.scale);
-            uint32_t w[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
+            const uint4 raw = W == 1 ? q_chunk(i) : qraw[W == 1 ? 0 : i];
+            uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             if (F8) {
               float x[8], amax = 0.f;
 #pragma unroll
@@ -985,11 +1009,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
               mult *= (a.kv.k_scale ? __ldg(a.kv.k_scale + h) : 1.f) *
                       __uint_as_float((uint32_t)(127 - e) << 23);
             }
-            if (QP * kThreads == C::kRows * LQ || r < C::kRows) {
+            if (QP * TT == C::kRows * LQ || r < C::kRows) {
               if (part == 0) {
                 // a masked score (-inf) times the factor must stay one: at least FLT_MIN
                 s_mult[r] = use_cap ? mult / a.softcap : fmaxf(mult * kLog2e, FLT_MIN);
-                s_one[r] = 1.f;
+                s_one[r] = 1.f;  // every team's the same
                 s_end[r] = end0 + (row0 + r) / a.group;
               }
               // a negative scale is carried by the queries, so that the factor is not negative
@@ -1011,10 +1035,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           last = __reduce_max_sync(~0u, last);
           if (lane == 0) s_last[warp] = last;
         }
-        __syncthreads();
+        sync();
         if (listed) {
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) last = max(last, s_last[w]);
+          for (int w = 0; w < W; ++w) last = max(last, s_last[team * W + w]);
           sb = min(sb, sa + last / C::kUnit + (last < 0 ? 0 : 1));
         }
 
@@ -1032,7 +1056,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             const uint32_t dst = ring_u + put * C::kHalf;
             src0 += cl * 16;
             if (listed) {
-              const uint32_t* e0 = tb_ + t * C::kUnit + warp * KS + rl;
+              const uint32_t* e0 = tb_ + t * C::kUnit + tw * KS + rl;
 #pragma unroll
               for (int j = 0; j < KS / RPI; ++j) {
                 const uint32_t e = e0[j * RPI];
@@ -1044,7 +1068,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
               const int64_t ts = is_v ? v_ts : k_ts;
 #pragma unroll
               for (int gr = 0; gr < KS / 16; ++gr) {
-                const int grp = t * (C::kUnit / 16) + warp * (KS / 16) + gr;
+                const int grp = t * (C::kUnit / 16) + tw * (KS / 16) + gr;
                 const uint32_t e = tb_[grp];
                 const int key = (sp.t0 + sa) * C::kUnit + grp * 16 + rl;
                 const uint8_t* src = src0 + (e != kNone ? (uint64_t)e * a.off_unit + rl * ts : 0);
@@ -1082,7 +1106,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           get = get + 1 == NS ? 0 : get + 1;
           issue(2 * t + NS);
 
-          const int tile0 = t * C::kUnit + warp * KS;  // within the sub-range
+          const int tile0 = t * C::kUnit + tw * KS;  // within the sub-range
           const int key0 = (sp.t0 + sa) * C::kUnit + tile0;
           bool whole;  // every key of the tile is seen by every row
           if (listed) {
@@ -1116,29 +1140,29 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         claimed = true;
         claim();  // while the sums are joined
       }
-      __syncthreads();
+      sync();
       const bool complete = ta == 0 && tb == units;
       // partial 2 s is a segment's first part, 2 s + 1 its last; an item's parts are its
       // first segment's last (or only) part, then the following segments' first parts
       const int item_end = u + cost - stop;  // in the cut's units
       const int part = 2 * seg + (first_item ? 0 : 1);
-      if (a.split && ta == 0 && tid == kThreads - 1)
+      if (split && ta == 0 && tid == TT - 1)
         a.desc[req * HR + hr] =
             make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(item_end - 1) - seg + 1);
       constexpr int QPR = D / 4;  // float4 quads per row
-      for (int i = tid; i < rows * QPR; i += kThreads) {
+      for (int i = tid; i < rows * QPR; i += TT) {
         const int r = i / QPR, d = (i % QPR) * 4;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_ml[w][r].x);
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[team * W + w][r].x);
         float lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 ml = s_ml[w][r];
+        for (int w = 0; w < W; ++w) {
+          const float2 ml = s_ml[team * W + w][r];
           if (ml.x == -INFINITY && ml.y == 0.f) continue;  // the warp saw nothing of this row
           const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
-          const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kRing + (r * C::kPitch + d) * 4);
+          const float4 x = *reinterpret_cast<const float4*>(smem + (team * W + w) * C::kRing + (r * C::kPitch + d) * 4);
           lsum += ml.y * f;
           acc.x += x.x * f;
           acc.y += x.y * f;
@@ -1166,11 +1190,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           if (d == 0) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(mx, lsum);
         }
       }
-      __syncthreads();  // the rings, the table and the query rows are refilled next
+      sync();  // the rings, the table and the query rows are refilled next
 
       req = req_next;
     }
-    if (!a.split || cut.K == 0) break;
+    if (!split || cut.K == 0) break;
     if (!claimed) {
       claim();
       __syncthreads();
@@ -1180,14 +1204,18 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   }
 }
 
-template <int D, int CT, int NT>
-cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, CT, NT>;
-  auto kern = a.topk_idx ? paged_attn_kernel<D, CT, NT, true> : paged_attn_kernel<D, CT, NT, false>;
+template <int D, int CT, int NT, int W>
+cudaError_t launch_team(const AttnArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, CT, NT, W>;
+  auto kern = a.topk_idx ? paged_attn_kernel<D, CT, NT, true, W> : paged_attn_kernel<D, CT, NT, false, W>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(a.grid), dim3(kThreads), C::kSmem,
-                          stream, a);
+  return launch_dependent(kern, dim3(a.grid), dim3(kThreads), C::kSmem, stream, a);
+}
+
+template <int D, int CT, int NT>
+cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+  return a.warp_items ? launch_team<D, CT, NT, 1>(a, stream) : launch_team<D, CT, NT, kWarps>(a, stream);
 }
 
 template <int D, int CT>

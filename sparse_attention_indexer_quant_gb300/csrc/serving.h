@@ -107,6 +107,7 @@ struct AttnArgs {
   int32_t one_table;  // k and v have the same page and token strides
   int32_t q_bf16;     // type of q and out
   int32_t split;      // 0: one CTA per item, no join
+  int32_t warp_items; // a warp per item (then split = 0)
   int32_t grid;
   idx_device_errors* errors;
 };
@@ -115,18 +116,19 @@ struct AttnArgs {
 constexpr int attn_row_tiles(int head_dim, int rows) {
   return rows <= 8 ? 1 : (rows <= 16 || head_dim > 128 ? 2 : 4);
 }
-constexpr int attn_keys_per_tile(int head_dim, int cache_dtype, int nt) {
-  return head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) >= 256 || nt == 4 ? 16 : 32;
+// keys of a warp's tile, with eight warps or one sharing an item
+constexpr int attn_keys_per_tile(int head_dim, int cache_dtype, int nt, int warps) {
+  return head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) >= 256 || nt == 4 || warps == 1 ? 16 : 32;
 }
 // Resident CTAs per SM: two where the sums take at most 64 registers a thread
 // and three half stages fit 12 KB of shared memory a warp.
 constexpr int attn_occupancy(int head_dim, int cache_dtype, int nt) {
   return head_dim * nt <= 256 && 3 * head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) *
-                                         attn_keys_per_tile(head_dim, cache_dtype, nt) <= 12288 ? 2 : 1;
+                                         attn_keys_per_tile(head_dim, cache_dtype, nt, 8) <= 12288 ? 2 : 1;
 }
 // keys a CTA handles at a time (the unit in which an item's length is split)
 constexpr int attn_unit_keys(int head_dim, int cache_dtype, int nt) {
-  return 8 * attn_keys_per_tile(head_dim, cache_dtype, nt);
+  return 8 * attn_keys_per_tile(head_dim, cache_dtype, nt, 8);
 }
 cudaError_t launch_attn_bf16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_fp16(const AttnArgs& a, cudaStream_t stream);

@@ -422,8 +422,15 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   const int64_t items = (int64_t)(topk_idx ? B * next_n : B) * kv->heads * a.row_tiles;
   int64_t ctas = (int64_t)sms * idx::attn_occupancy(D, kv->dtype, nt);
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
-  a.split = units > 2;
-  const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
+  // Many short items: a warp each.  2048 items of 20 - 100 keys 15.9 us, with a
+  // CTA each 37.0; 1024 of 100 - 250 keys 23.8 and 27.0; 2048 of 300 - 500 keys
+  // 71.6 and 78.1; but 512 of 250 keys 22.9 and 14.5 (too few warps to hide the
+  // latency of a long item).
+  a.warp_items = (keys <= 256 && items >= 4 * (int64_t)sms) || (keys <= 512 && items >= 12 * (int64_t)sms);
+  a.split = units > 2 && !a.warp_items;
+  const int64_t grid = a.split        ? (units * items < ctas ? units * items : ctas)
+                       : a.warp_items ? (items + 7) / 8
+                                      : items;
   if ((units + 64) * items > INT32_MAX || items * a.part_rows > INT32_MAX)
     return fail(IDX_ERR_INVALID_ARG, "%lld query row tiles of up to %lld keys: too much for one call",
                 (long long)items, (long long)keys);

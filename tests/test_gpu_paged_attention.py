@@ -169,6 +169,33 @@ def test_many_requests(idx):
     check(idx, make(lens[:150], 4, 4, 128, "bf16", "e4m3", page=16, k=64, next_n=2))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"),
+                                         ("fp16", "e4m3")])
+@pytest.mark.parametrize("group", [1, 5, 12, 20, 40])
+def test_many_short_requests(idx, D, dtype, cache, group):
+    """Enough short items that each is a single warp's."""
+    r = np.random.default_rng(D + group)
+    lens = [0, 1, 15, 16, 17, 31, 32, 33, 255, 256] + r.integers(0, 257, 310).tolist()
+    check(idx, make(lens, 2 * group, 2, D, dtype, cache, page=16, seed=group))
+
+
+@pytest.mark.parametrize("D,cache,order", [(64, "bf16", "nhd"), (128, "e4m3", "hnd"),
+                                           (128, "bf16", "nhd"), (256, "bf16", "hnd")])
+def test_many_short_rows_in_every_form(idx, D, cache, order):
+    r = np.random.default_rng(D)
+    lens = [0, 1, 2, 3, 100] + r.integers(0, 200, 215).tolist()
+    check(idx, make(lens, 9, 3, D, "bf16", cache, page=32, next_n=3, order=order), softcap=20.0)
+    check(idx, make(lens, 9, 3, D, "bf16", cache, page=32, next_n=3, order=order), window=37,
+          scale=-0.1)
+    check(idx, make(lens, 9, 3, D, "bf16", cache, page=64, next_n=2, k=100, order=order))
+    check(idx, make(lens, 9, 3, D, "bf16", cache, page=16, next_n=1, k=256, order=order, hole=0.0))
+    check(idx, make(lens, 9, 3, D, "bf16", cache, page=128, next_n=2, k=1, order=order))
+    p = make(lens, 9, 3, D, "bf16", cache, page=16, order=order)
+    p["bt"][4, 2], p["bt"][4, 3] = -7, 10**7   # 100 tokens: pages 0 - 6
+    check(idx, p, bad=2)
+
+
 def test_ranges_longer_than_the_page_table_in_shared_memory(idx):
     """A CTA's range of more than 32768 keys, and of more than 2048 listed
     positions: 320 kv heads that are one head seen again (head stride 0)."""
