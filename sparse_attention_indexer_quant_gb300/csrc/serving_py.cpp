@@ -145,6 +145,10 @@ PyObject* guarded(F&& f) {
   return nullptr;
 }
 
+// A dimension of one entry has no stride to speak of: whatever torch says there
+// need not be aligned.
+int64_t stride_of(const Tensor& t, int64_t dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
 int dtype_of(const Tensor& q) {
   if (q.scalar_type() == ScalarType::BFloat16) return IDX_BF16;
   if (q.scalar_type() == ScalarType::Half) return IDX_FP16;
@@ -178,12 +182,12 @@ idx_kv_cache kv_of(PyObject* ko, PyObject* vo, PyObject* kso, PyObject* vso) {
   kv.heads = (int32_t)k.size(1);
   kv.page_size = (int32_t)k.size(2);
   kv.head_dim = (int32_t)k.size(3);
-  kv.k_block_stride = k.stride(0);
-  kv.k_head_stride = k.stride(1);
-  kv.k_token_stride = k.stride(2);
-  kv.v_block_stride = v.stride(0);
-  kv.v_head_stride = v.stride(1);
-  kv.v_token_stride = v.stride(2);
+  kv.k_block_stride = stride_of(k, 0);
+  kv.k_head_stride = stride_of(k, 1);
+  kv.k_token_stride = stride_of(k, 2);
+  kv.v_block_stride = stride_of(v, 0);
+  kv.v_head_stride = stride_of(v, 1);
+  kv.v_token_stride = stride_of(v, 2);
   kv.k_scale = maybe<const float>(kso, ScalarType::Float, "k_scale", kv.heads,
                                   "have one entry per kv head");
   kv.v_scale = maybe<const float>(vso, ScalarType::Float, "v_scale", kv.heads,
@@ -328,8 +332,8 @@ PyObject* qk_norm_rope_insert(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (out.sizes() != q.sizes()) value_error("q_out must have q's shape");
     }
     check("idx_qk_norm_rope_insert",
-          idx_qk_norm_rope_insert(ptr(q), q.stride(0), q.stride(1), ptr(k), k.stride(0), k.stride(1),
-                                  ptr(v), v.stride(0), v.stride(1), N, (int32_t)q.size(1), dtype, qw,
+          idx_qk_norm_rope_insert(ptr(q), stride_of(q, 0), stride_of(q, 1), ptr(k), stride_of(k, 0), stride_of(k, 1),
+                                  ptr(v), stride_of(v, 0), stride_of(v, 1), N, (int32_t)q.size(1), dtype, qw,
                                   kw, (float)real(a[5]), pos, cs, sn, num_pos, rot, inter,
                                   ptr<int64_t>(slots), ptr(out), &kv, errors_of(a[17]), stream()));
     if (a[16] != Py_None) {
@@ -393,7 +397,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const float scale = a[6] == Py_None ? (float)(1.0 / sqrt((double)dim)) : (float)real(a[6]);
     check("idx_paged_attention",
-          idx_paged_attention(ptr(q), q.stride(0), q.stride(1), dtype, (int32_t)B, next_n,
+          idx_paged_attention(ptr(q), stride_of(q, 0), stride_of(q, 1), dtype, (int32_t)B, next_n,
                               (int32_t)Hq, &kv, ptr<int32_t>(bt), (int32_t)bt.size(1),
                               ptr<int32_t>(lens), topk, (int32_t)k, scale, (float)real(a[7]),
                               int32(a[8], "window"), ptr(out),

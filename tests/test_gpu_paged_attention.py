@@ -347,6 +347,24 @@ def test_graph_replays_read_their_buffers_afresh(idx):
         su.check_attention(out, lse, ref, 128, torch.bfloat16, what=str(now))
 
 
+def test_strides_of_single_entries_do_not_matter(idx):
+    """One request, one kv head, one block: their strides are anything."""
+    D = 64
+    p = make([16], 1, 1, D, page=16)
+    want, _ = call(idx, p)
+    q = torch.empty(1, 1, D + 3, dtype=torch.bfloat16, device="cuda")[:, :, :D]
+    kc, vc = (torch.empty(16 * D, dtype=torch.bfloat16, device="cuda")
+              .as_strided((1, 1, 16, D), (16 * D + 5, 16 * D + 3, D, 1)) for _ in range(2))
+    assert q.stride(0) % 8 and kc.stride(0) % 8
+    q.copy_(p["q"])
+    blk = int(p["bt"][0, 0])
+    kc.copy_(p["kc"][blk:blk + 1])
+    vc.copy_(p["vc"][blk:blk + 1])
+    out = idx.paged_attention(q, kc, vc, i32([[0]]), i32([16]))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_no_requests(idx):
     kc, vc = idx.new_kv_cache(2, 2, 64)
     out = idx.paged_attention(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), kc, vc,
