@@ -45,7 +45,7 @@ __device__ __forceinline__ void load8(const float* p, bool vec, float (&x)[8]) {
 __device__ __forceinline__ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <int D, bool BF16, bool CACHE8, bool PAIRS, int VPT>
-__global__ void __launch_bounds__(kThreads, 8) kv_insert_kernel(
+__global__ void __launch_bounds__(kThreads, CACHE8 ? 9 : 8) kv_insert_kernel(
     const __grid_constant__ KvInsertArgs a, int q_groups, int k_groups) {
   constexpr int kLanes = D / 8;
   const unsigned part = threadIdx.x % kLanes;
@@ -70,6 +70,18 @@ __global__ void __launch_bounds__(kThreads, 8) kv_insert_kernel(
   pdl_launch_dependents();
   pdl_wait();  // inputs may come from the previous kernel
 
+  int64_t slot = -1;
+  int32_t pos = 0;
+  auto load_place = [&]() {
+    if (live) {
+      slot = __ldg(a.slots + t);
+      if (a.rot_dim > 0) pos = __ldg(a.positions + t);
+    }
+  };
+  // the table's row waits for the position: where it is long (16 values a lane)
+  // the position goes first (147 us, after the heads 153), where short it does
+  // not pay (136 and 134)
+  if (!PAIRS) load_place();
   const int64_t hs = kind == kQuery ? a.q_hs : (kind == kKey ? a.k_hs : a.v_hs);
   const uint16_t* src = kind == kQuery ? static_cast<const uint16_t*>(a.q) + t * a.q_ts
                         : kind == kKey ? static_cast<const uint16_t*>(a.k) + t * a.k_ts
@@ -79,12 +91,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv_insert_kernel(
 #pragma unroll
   for (int u = 0; u < VPT; ++u)
     raw[u] = u < n ? *reinterpret_cast<const uint4*>(src + u * hs) : make_uint4(0, 0, 0, 0);
-  int64_t slot = -1;
-  int32_t pos = 0;
-  if (live) {
-    slot = __ldg(a.slots + t);
-    if (a.rot_dim > 0) pos = __ldg(a.positions + t);
-  }
+  if (PAIRS) load_place();
   const bool pos_ok = a.rot_dim == 0 || (pos >= 0 && pos < a.num_pos);
   const bool slot_ok = slot >= 0 && slot < (a.kv.num_blocks << a.page_shift);
   if (live && kind == kQuery && h0 == 0 && part == 0 && (!pos_ok || (slot != -1 && !slot_ok)))
