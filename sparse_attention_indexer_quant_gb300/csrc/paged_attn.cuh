@@ -819,7 +819,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         req = x / weight(list_units);
         base = req * weight(list_units);
       } else {
-        int before = 0;  // weights of the requests before this round's
+        int before = 0;  // weights of the requests before these
         if (tid == 0) s_req = -1;
         for (int b0 = 0; b0 < reqs; b0 += kThreads) {
           const int b = b0 + tid;
@@ -985,7 +985,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll(W == 1 ? 2 : QP)
           for (int i = 0; i < QP; ++i) {
             const int r = (i * TT + tid) / LQ, part = tid % LQ;
-            float mult = fabsf(a.scale);
+            float mult = a.scale;
             const uint4 raw = W == 1 ? q_chunk(i) : qraw[W == 1 ? 0 : i];
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             if (F8) {
@@ -1012,19 +1012,19 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             if (QP * TT == C::kRows * LQ || r < C::kRows) {
               if (part == 0) {
                 // a masked score (-inf) times the factor must stay one: at least FLT_MIN
-                s_mult[r] = use_cap ? mult / a.softcap : fmaxf(mult * kLog2e, FLT_MIN);
+                s_mult[r] = use_cap ? fabsf(mult) / a.softcap : fmaxf(fabsf(mult) * kLog2e, FLT_MIN);
                 s_one[r] = 1.f;  // every team's the same
                 s_end[r] = end0 + (row0 + r) / a.group;
               }
-              // a negative scale is carried by the queries, so that the factor is not negative
-              const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+              // a factor's sign is carried by the queries, and so is a NaN (of a key scale)
+              const uint32_t flip = mult < 0.f ? 0x80008000u : 0u, nan = mult != mult ? 0x7FFF7FFFu : 0u;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 int d = part * 8 + 2 * j;
                 // 8-bit keys come from ldmatrix four codes a lane: dimension 4c+i of a
                 // 16-block sits at k index 2c+i (i < 2) or 8+2c+i-2
                 if (F8) d = (d & ~15) + ((d & 2) ? 8 : 0) + ((d & 15) >> 2) * 2;
-                *reinterpret_cast<uint32_t*>(q_sm + swz<D * 2>(r, d >> 3) + (d & 7) * 2) = w[j] ^ flip;
+                *reinterpret_cast<uint32_t*>(q_sm + swz<D * 2>(r, d >> 3) + (d & 7) * 2) = (w[j] ^ flip) | nan;
               }
             }
           }

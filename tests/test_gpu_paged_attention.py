@@ -277,6 +277,32 @@ def test_large_scores(idx):
     check(idx, p, scale=2.0 ** 100)
 
 
+@pytest.mark.parametrize("softcap", [0.0, 4.0])
+@pytest.mark.parametrize("next_n,k", [(1, 0), (9, 0), (1, 40)])
+def test_key_scales_of_either_sign(idx, softcap, next_n, k):
+    """A head's negative scale turns its scores around, also under a negative
+    softmax scale; a scale of zero makes all of a row's weights equal."""
+    p = make([300, 1200, 9], 6, 3, 128, "bf16", "e4m3", next_n=next_n, k=k)
+    ks = p["ks"].clone()
+    p["ks"] = ks * torch.tensor([1.0, -1.0, 0.0])
+    p["k64"] = p["k64"] * np.array([1.0, -1.0, 0.0])[None, :, None, None]
+    for scale in (0.1, -0.1):
+        check(idx, p, scale=scale, softcap=softcap)
+
+
+def test_a_key_scale_of_nan_is_not_passed_over(idx):
+    p = make([300, 0], 4, 2, 128, "bf16", "e4m3")
+    clean, clean_lse = call(idx, p)
+    p["ks"] = torch.tensor([float("nan"), p["ks"][1]])
+    for softcap in (0.0, 4.0):
+        out, lse = call(idx, p, softcap=softcap)
+        torch.cuda.synchronize()
+        assert torch.isnan(out[0, :2]).all() and torch.isnan(lse[0, :2]).all()
+        assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()  # sees nothing
+        if not softcap:
+            assert torch.equal(out[0, 2:], clean[0, 2:]) and torch.equal(lse[0, 2:], clean_lse[0, 2:])
+
+
 def test_results_do_not_depend_on_the_run(idx):
     p = make([20000, 3000, 1], 8, 2, 128)
     a = call(idx, p)
