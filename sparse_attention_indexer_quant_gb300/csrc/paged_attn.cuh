@@ -19,11 +19,11 @@
 //
 // Arithmetic.  o = sum_s p_s v_s / sum_s p_s with p_s = 2^(x_s - m), one pass
 // with a running reference m per row that is raised (and the sums rescaled)
-// only when a score passes it by more than 2^8, which fp32 sums hold easily:
-// most tiles need one vote instead of shuffle reductions.  Scores and sums are
-// fp32 accumulators of m16n8k16 products.  Up to eight rows: keys (then value
-// dimensions) on M, query rows on N, so that eight rows fill a tile: S^T =
-// K Q^T, then O^T = V^T P^T, P passing from one product's result layout to the
+// only when a score passes the highest at the last raise by more than 2^8, which
+// fp32 sums hold easily: most tiles need one vote instead of shuffle reductions.
+// Scores and sums are fp32 accumulators of m16n8k16 products.  Up to eight rows:
+// keys (then value dimensions) on M, query rows on N, so that eight rows fill a
+// tile: S^T = K Q^T, then O^T = V^T P^T, P passing from one product's result layout to the
 // other's operand layout by a register transpose (movmatrix).  More rows: query
 // rows on M.  p goes into the second product as two 16-bit terms, hi = round(p)
 // and lo = round(p - hi): one term's rounding (2^-9 in bf16) would be as large
@@ -64,7 +64,12 @@ constexpr int kTab = 2048;  // words of the table of resolved page groups / list
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.f;  // log2 of how far a score may pass the reference
+constexpr float kSlack = 8.f;  // log2 of how far a score may pass the highest at the last raise
+// log2 of the weight that a raise gives the highest score: with fp16 operands as
+// high as their range allows (2^15 after the slack), since what lies under 2^-25
+// is lost: 2^-32 of the highest weight and less
+template <bool MB>
+constexpr float kLift = MB ? 0.f : 7.f;
 
 template <int D, int CT>
 constexpr int row_bytes() { return D * (CT == IDX_E4M3 ? 1 : 2); }
@@ -362,12 +367,12 @@ struct KeysOnM {
 #pragma unroll
       for (int kg = 1; kg < KS / 16; ++kg) x = fmaxf(x, fmaxf(s[kg][e], s[kg][2 + e]));
       mx[e] = x * f[e];
-      raise = raise || mx[e] > m[e] + kSlack;
+      raise = raise || mx[e] > m[e] + (kLift<MB> + kSlack);
     }
     if (__any_sync(~0u, raise)) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(mx[e], m[e]);
+        float x = fmaxf(mx[e] - kLift<MB>, m[e]);
         x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
         x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
         x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
@@ -571,14 +576,14 @@ struct RowsOnM {
 #pragma unroll
         for (int i = 1; i < KS / 8; ++i) x = fmaxf(x, fmaxf(s[mt][i][2 * e], s[mt][i][2 * e + 1]));
         mx[mt][e] = x * f.f[mt][e];
-        raise = raise || mx[mt][e] > m[mt][e] + kSlack;
+        raise = raise || mx[mt][e] > m[mt][e] + (kLift<MB> + kSlack);
       }
     if (__any_sync(~0u, raise)) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(mx[mt][e], m[mt][e]);
+          float x = fmaxf(mx[mt][e] - kLift<MB>, m[mt][e]);
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
           const float w = m[mt][e] == -INFINITY ? 0.f : ex2(m[mt][e] - x);

@@ -303,6 +303,40 @@ def test_a_key_scale_of_nan_is_not_passed_over(idx):
             assert torch.equal(out[0, 2:], clean[0, 2:]) and torch.equal(lse[0, 2:], clean_lse[0, 2:])
 
 
+@pytest.mark.parametrize("n", [300, 5000])
+@pytest.mark.parametrize("dtype,cache,group", [("fp16", "fp16", 4), ("fp16", "e4m3", 4),
+                                               ("bf16", "e4m3", 16), ("bf16", "bf16", 4)])
+def test_few_high_scores_among_many_low_ones(idx, dtype, cache, group, n):
+    """Every sixteenth key has a weight near 1 and a value of zero; the result
+    is made of the others, whose weights are near 2^-24.  With fp16 operands
+    both terms of a weight lie on fp16's smallest grid there: off by half a step
+    of 2^-31 of the highest weight."""
+    p = make([n], group, 1, 64, dtype, cache, page=16, scales=False)
+    pages = len(p["bt"][0])
+    q = torch.zeros(p["q"].shape)
+    q[:, :, 0] = 16.0
+    r = np.random.default_rng(1)
+    keys = torch.tensor(-1.0 + r.integers(-4, 5, pages * 16) / 64.0)
+    vals = torch.full((pages * 16,), 256.0)
+    keys[::16] = 0.0
+    vals[::16] = 0.0
+    kf, vf = (torch.zeros(p["kc"].shape) for _ in range(2))
+    kf[torch.tensor(p["bt"][0].astype(np.int64)), 0, :, 0] = keys.view(-1, 16).float()
+    vf[torch.tensor(p["bt"][0].astype(np.int64)), 0] = vals.view(-1, 16, 1).float()
+    p["q"], p["kc"], p["vc"] = q.to(p["q"].dtype), kf.to(p["kc"].dtype), vf.to(p["vc"].dtype)
+    scale = 1.04
+    out, lse = call(idx, p, scale=scale)
+    torch.cuda.synchronize()
+    ref = su.ref_attention(su.to64(p["q"]), su.to64(p["kc"]), su.to64(p["vc"]), p["bt"], p["lens"],
+                           1, float(np.float32(scale)))
+    tol, tol_lse = su.attention_tols(*ref, 64, p["dtype"])
+    assert 1e-4 < ref[0].min() and ref[0].max() < 1e-3
+    if cache != "bf16":
+        tol = tol + 15 * 256 * 2.0 ** -32
+    assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_lse).all()
+
+
 def test_results_do_not_depend_on_the_run(idx):
     p = make([20000, 3000, 1], 8, 2, 128)
     a = call(idx, p)
