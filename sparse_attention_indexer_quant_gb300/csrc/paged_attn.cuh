@@ -2,10 +2,13 @@
 //
 // Work.  An item is one kv head of one request with its query rows (next_n
 // tokens times the heads of the group; with a selection, one token's group),
-// up to 8 * NT of them.  Many short items are taken by a warp each; else a CTA
-// of eight warps shares an item.  Its keys are cut into units of 8 * KS (64 KB
-// of cache for most shapes), numbered item by item over the whole batch, and the units
-// into segments (see Cut).  With R resident CTAs the first R segments take
+// up to 8 * NT of them.  An item is taken whole by a team of W = 8, 4, 2 or 1
+// warps of a CTA, the blocks' order left to the hardware: long items by whole
+// CTAs, short ones by few warps, so that one team sets an item up while others
+// stream.  Where that would leave SMs idle (few or long items; the caller
+// estimates both) the items are split: their keys are cut into units of 8 * KS
+// (64 KB of cache for most shapes), numbered item by item over the whole batch,
+// and the units into segments (see Cut).  With R resident CTAs the first R segments take
 // three quarters of the units, one segment per CTA; the rest are cut into
 // levels of R segments of 1/8, 1/16, ... that the CTAs claim from a counter as
 // they finish: with equal shares alone the first CTA was done after 614 us and
@@ -74,10 +77,10 @@ constexpr float kLift = MB ? 0.f : 7.f;
 template <int D, int CT>
 constexpr int row_bytes() { return D * (CT == IDX_E4M3 ? 1 : 2); }
 
-// W warps share an item: the CTA's eight, or one (short items, eight a CTA).
+// W warps (a team) share an item; a CTA has eight warps.
 template <int D, int CT, int NT, int W>
 struct Cfg {
-  static_assert(W == kWarps || W == 1, "");
+  static_assert(W == kWarps || W == 4 || W == 2 || W == 1, "");
   static constexpr bool kF8 = CT == IDX_E4M3;
   static constexpr bool kMmaBf16 = CT == IDX_BF16;
   static constexpr int kRowB = row_bytes<D, CT>();
@@ -89,17 +92,17 @@ struct Cfg {
   static constexpr int kHalf = kRowB * kKS;  // bytes of a half stage
   // two CTAs per SM where 128 registers a thread hold the accumulators
   static constexpr int kOcc = attn_occupancy(D, CT, NT);
-  static constexpr int kPitch = W == 1 ? D : D + 4;  // floats of a row of the merge buffer
+  static constexpr int kPitch = W < kWarps ? D : D + 4;  // floats of a row of the merge buffer
   static constexpr int kSums = kRows * kPitch * 4;
-  // a warp's ring: all the room there is, or with an item per warp two half
-  // stages, 8 KB or the sums
-  static constexpr int kMinRing = kSums > 8192 ? (kSums > 2 * kHalf ? kSums : 2 * kHalf)
-                                               : (2 * kHalf > 8192 ? 2 * kHalf : 8192);
-  static constexpr int kStages = W == 1 ? kMinRing / kHalf : (kOcc == 2 ? 12288 : 24576) / kHalf;
-  static constexpr int kRing = kStages * kHalf;
   static constexpr int kTeams = kWarps / W;
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kTabWords = kTab / kTeams;
+  // halved where three half stages would not fit beside it
+  static constexpr int kTabWords = (W == 2 || W == 4 ? kTab / 2 : kTab) / kTeams;
+  // a warp's ring: 12 KB, or 24 with one CTA an SM, or what the teams' query rows leave
+  static constexpr int kMost = kOcc == 2 ? 12288 : 24576;
+  static constexpr int kRoom = (222 * 1024 / kOcc - kTeams * (kQBytes + kTabWords * 4)) / kWarps;
+  static constexpr int kStages = (kRoom < kMost ? kRoom : kMost) / kHalf;
+  static constexpr int kRing = kStages * kHalf;
   static constexpr int kSmem = kWarps * kRing + kTeams * (kQBytes + kTabWords * 4);
   static_assert(kSums <= kRing, "a warp's sums fit its ring");
   static_assert(kStages >= 2 && kRing % kHalf == 0, "");
@@ -708,9 +711,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the team that shares an item, and this thread's place in it
   constexpr int TT = 32 * W;
-  const int team = W == 1 ? warp : 0, tw = W == 1 ? 0 : warp, tid = W == 1 ? lane : (int)threadIdx.x;
+  const int team = warp / W, tw = warp % W, tid = (int)threadIdx.x % TT;
   auto sync = [&]() {
-    if (W == 1) __syncwarp(); else __syncthreads();
+    if (W == 1) __syncwarp();
+    else if (W == kWarps) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TT) : "memory");
   };
   float* s_mult = s_mults[team];
   int* s_end = s_ends[team];
@@ -759,7 +764,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   }
   const Cut cut(split ? U : (int)gridDim.x, (int)gridDim.x);
   // q > 0: units of a piece
-  int q = 0, segments = W == 1 ? reqs * HR : cut.segments();
+  int q = 0, segments = W < kWarps ? reqs * HR : cut.segments();
   if (split && cut.K == 0) {
     const int real = U - reqs * HR * kSetup;
     const int q0 = (real + (int)gridDim.x - 1) / (int)gridDim.x, step = max(1, q0 / 12);
@@ -807,7 +812,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
     }
   };
-  for (int seg = W == 1 ? blockIdx.x * kWarps + warp : blockIdx.x; seg < segments;) {
+  for (int seg = W < kWarps ? blockIdx.x * C::kTeams + team : blockIdx.x; seg < segments;) {
     // ---- the segment's units [u0, u1), and the request its first unit belongs to
     int u0, u1, base, req;  // base: first unit of request `req`
     if (!split) {  // one team per item; units are counted from its request's first
@@ -919,10 +924,10 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
                               (int64_t)(h * a.group + rr % a.group) * a.q_hs;
         return __ldg(reinterpret_cast<const uint4*>(src) + tid % LQ);
       };
-      uint4 qraw[W == 1 ? 1 : QP];
-      if (W > 1) {
+      uint4 qraw[W < kWarps ? 1 : QP];
+      if (W == kWarps) {
 #pragma unroll
-        for (int i = 0; i < QP; ++i) qraw[W == 1 ? 0 : i] = q_chunk(i);
+        for (int i = 0; i < QP; ++i) qraw[W < kWarps ? 0 : i] = q_chunk(i);
       }
 
       typename TileOf<D, CT, NT, KS>::type tile;
@@ -987,11 +992,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         }
         if (sa == ta) {
           // ---- query rows to shared memory
-#pragma unroll(W == 1 ? 2 : QP)
+#pragma unroll(W < kWarps && QP > 2 ? 2 : QP)
           for (int i = 0; i < QP; ++i) {
             const int r = (i * TT + tid) / LQ, part = tid % LQ;
             float mult = a.scale;
-            const uint4 raw = W == 1 ? q_chunk(i) : qraw[W == 1 ? 0 : i];
+            const uint4 raw = W < kWarps ? q_chunk(i) : qraw[W < kWarps ? 0 : i];
             uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
             if (F8) {
               float x[8], amax = 0.f;
@@ -1220,7 +1225,12 @@ cudaError_t launch_team(const AttnArgs& a, cudaStream_t stream) {
 
 template <int D, int CT, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  return a.warp_items ? launch_team<D, CT, NT, 1>(a, stream) : launch_team<D, CT, NT, kWarps>(a, stream);
+  switch (a.team) {
+    case 1: return launch_team<D, CT, NT, 1>(a, stream);
+    case 2: return launch_team<D, CT, NT, 2>(a, stream);
+    case 4: return launch_team<D, CT, NT, 4>(a, stream);
+  }
+  return launch_team<D, CT, NT, kWarps>(a, stream);
 }
 
 template <int D, int CT>

@@ -106,8 +106,8 @@ struct AttnArgs {
   uint32_t off_unit;  // off_unit, and fits 32 bits in that unit
   int32_t one_table;  // k and v have the same page and token strides
   int32_t q_bf16;     // type of q and out
-  int32_t split;      // 0: one CTA per item, no join
-  int32_t warp_items; // a warp per item (then split = 0)
+  int32_t split;      // 0: items whole, no join
+  int32_t team;       // warps that share an item: 8, 4, 2 or 1 (fewer than 8 only with split = 0)
   int32_t grid;
   idx_device_errors* errors;
 };
@@ -116,9 +116,9 @@ struct AttnArgs {
 constexpr int attn_row_tiles(int head_dim, int rows) {
   return rows <= 8 ? 1 : (rows <= 16 || head_dim > 128 ? 2 : 4);
 }
-// keys of a warp's tile, with eight warps or one sharing an item
+// keys of a warp's tile, with `warps` warps sharing an item
 constexpr int attn_keys_per_tile(int head_dim, int cache_dtype, int nt, int warps) {
-  return head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) >= 256 || nt == 4 || warps == 1 ? 16 : 32;
+  return head_dim * (cache_dtype == IDX_E4M3 ? 1 : 2) >= 256 || nt == 4 || warps < 8 ? 16 : 32;
 }
 // Resident CTAs per SM: two where the sums take at most 64 registers a thread
 // and three half stages fit 12 KB of shared memory a warp.

@@ -109,6 +109,55 @@ int common_shift(int64_t x, int64_t y) {
   return s;
 }
 
+// Warps that share an item: 8 (a CTA), 4, 2 or 1, or 0: items split over all CTAs
+// and joined.  By an estimate of the call's microseconds for `items` items of up
+// to `bytes` bytes of cache: 5 to start; 2 to set an item up; 7.1 TB/s in all and
+// what a warp's ring and products let it stream, 6.2 GB/s, 12.4 where one CTA an
+// SM has rings twice as long, 5.2 with sixteen rows, 5 with 32; 15 to start, cut
+// and join.  Selected positions are as many for every item, and a last wave of few
+// items costs its whole time.  Contexts are taken to fill half of their room on
+// average, and the longest, which may come last, costs 0.4 of its time.  Over 256
+// measured cases of types, head layouts and lengths this choice takes 1.5 % more
+// time than the best of the five, and 12 % less than splitting all but the short
+// ones.
+//   us (8 heads, 8 rows of 128, bf16)     split   8 warps   4     2     1
+//   64 x 2048 selected                      94      88      89    98   177
+//   80 x 2048 selected                     113     121     144   119   180
+//   64 x 512 selected                       33      30      27    29    50
+//   128 x 128 selected                      23      23      16    13    16
+//   304 x 512 selected                     116     115     110   105   101
+//   128 contexts of 64 - 512                38      34      33    33    45
+//   128 of 128 - 1024                       58      52      56    59    81
+//   64 of 256 - 2048                        54      53      57    74   142
+//   256 of 2048                            308     297     304   300   309
+//   8 of 8192 - 32768                      103     203     517  1032  2130
+int attn_team(int64_t items, double bytes, bool listed, int ctas, int occ, int nt) {
+  const double setup = 2.0;
+  const double warp_rate = nt == 4 ? 5.0e3 : (nt == 2 ? 5.2e3 : 6.2e3) * (occ == 2 ? 1.0 : nt == 2 ? 1.5 : 2.0);
+  const double rate = fmin(7.1e6, ctas * 8 * warp_rate);
+  const double all = (double)items * bytes / rate * (listed ? 1.0 : 0.5);
+  double best = 15.0 + setup * (double)items / ctas + all;
+  int team = 0;
+  for (int w = 8; w >= 1; w /= 2) {
+    const int64_t slots = (int64_t)ctas * (8 / w);
+    const double alone = bytes / (w * warp_rate);
+    double t = 5.0;
+    if (listed) {
+      const int64_t waves = items / slots, rest = items % slots;
+      t += (double)waves * (setup + fmax((double)slots * bytes / rate, alone));
+      if (rest) t += setup + fmax((double)rest * bytes / rate, alone);
+    } else {
+      const double waves = (double)items / (double)slots;
+      t += setup * (waves > 1.0 ? waves + 0.5 : 1.0) + fmax(all + 0.4 * alone, alone);
+    }
+    if (t < best) {
+      best = t;
+      team = w;
+    }
+  }
+  return team;
+}
+
 bool attn_shape_ok(int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D) {
   return B >= 0 && B <= 65535 && next_n >= 1 && next_n <= 16 && Hkv >= 1 && Hkv <= 1024 &&
          Hq >= Hkv && Hq <= 4096 && Hq % Hkv == 0 && (D == 64 || D == 128 || D == 256) &&
@@ -413,24 +462,21 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   a.q_bf16 = dtype == IDX_BF16;
   a.errors = errors;
 
-  // Units an item can have at most, and the CTAs the device holds at once.
+  // Units an item can have at most, the CTAs the device holds at once, and how
+  // items are shared out.
   const int unit = idx::attn_unit_keys(D, kv->dtype, nt);
   int64_t keys = topk_idx ? topk : (int64_t)max_blocks * kv->page_size;
   if (!topk_idx && a.window > 0 && keys > (int64_t)a.window + next_n + unit)
     keys = (int64_t)a.window + next_n + unit;  // sight of all rows, first unit cut
   const int64_t units = (keys + unit - 1) / unit;
   const int64_t items = (int64_t)(topk_idx ? B * next_n : B) * kv->heads * a.row_tiles;
-  int64_t ctas = (int64_t)sms * idx::attn_occupancy(D, kv->dtype, nt);
+  const int occ = idx::attn_occupancy(D, kv->dtype, nt);
+  int64_t ctas = (int64_t)sms * occ;
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
-  // Many short items: a warp each.  2048 items of 20 - 100 keys 15.9 us, with a
-  // CTA each 37.0; 1024 of 100 - 250 keys 23.8 and 27.0; 2048 of 300 - 500 keys
-  // 71.6 and 78.1; but 512 of 250 keys 22.9 and 14.5 (too few warps to hide the
-  // latency of a long item).
-  a.warp_items = (keys <= 256 && items >= 4 * (int64_t)sms) || (keys <= 512 && items >= 12 * (int64_t)sms);
-  a.split = units > 2 && !a.warp_items;
-  const int64_t grid = a.split        ? (units * items < ctas ? units * items : ctas)
-                       : a.warp_items ? (items + 7) / 8
-                                      : items;
+  const int team = attn_team(items, (double)keys * D * 2 * elt, topk_idx != nullptr, (int)ctas, occ, nt);
+  a.split = units > 2 && team == 0;
+  a.team = team == 0 ? 8 : team;
+  const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : (items * a.team + 7) / 8;
   if ((units + 64) * items > INT32_MAX || items * a.part_rows > INT32_MAX)
     return fail(IDX_ERR_INVALID_ARG, "%lld query row tiles of up to %lld keys: too much for one call",
                 (long long)items, (long long)keys);

@@ -196,6 +196,36 @@ def test_many_short_rows_in_every_form(idx, D, cache, order):
     check(idx, p, bad=2)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype,cache", [("bf16", "bf16"), ("fp16", "fp16"), ("bf16", "e4m3"),
+                                         ("fp16", "e4m3")])
+@pytest.mark.parametrize("heads,group", [(20, 4), (20, 12), (20, 24), (35, 4), (35, 20), (70, 3),
+                                         (70, 11), (140, 1)])
+def test_items_of_few_warps(idx, D, dtype, cache, heads, group):
+    """400 to 2800 items of at most 96 keys, which teams of four, two or one
+    warps take."""
+    r = np.random.default_rng(heads + group)
+    lens = [0, 1, 15, 16, 17, 31, 32, 33, 63, 64, 65, 95, 96] + r.integers(0, 97, 7).tolist()
+    check(idx, make(lens, heads * group, heads, D, dtype, cache, page=32, seed=group))
+    check(idx, make(lens, heads * group, heads, D, dtype, cache, page=16, k=96, hole=0.1), softcap=9.0)
+
+
+@pytest.mark.parametrize("D,cache,next_n", [(64, "bf16", 1), (128, "bf16", 3), (128, "e4m3", 2),
+                                            (256, "bf16", 1)])
+def test_items_of_few_warps_in_every_form(idx, D, cache, next_n):
+    """Lists of several tables of a team, windows, orders, bad pages."""
+    r = np.random.default_rng(D)
+    lens = [0, 1, 700, 701, 1000] + r.integers(300, 1000, 15).tolist()
+    for heads, order in ((20 // next_n, "nhd"), (35, "hnd")):
+        check(idx, make(lens, 3 * heads, heads, D, "bf16", cache, page=64, next_n=next_n, k=700,
+                        order=order, hole=0.3))
+        check(idx, make(lens, 3 * heads, heads, D, "bf16", cache, page=16, next_n=next_n,
+                        order=order), window=77, scale=-0.1)
+        p = make(lens, 3 * heads, heads, D, "bf16", cache, page=64, next_n=next_n, order=order)
+        p["bt"][2, 2], p["bt"][2, 10] = -7, 10**7
+        check(idx, p, softcap=20.0, bad=2)
+
+
 def test_ranges_longer_than_the_page_table_in_shared_memory(idx):
     """A CTA's range of more than 32768 keys, and of more than 2048 listed
     positions: 320 kv heads that are one head seen again (head stride 0)."""
