@@ -96,10 +96,13 @@ struct Cfg {
   static constexpr int kSums = kRows * kPitch * 4;
   static constexpr int kTeams = kWarps / W;
   static constexpr int kQBytes = kRows * D * 2;
-  // halved where three half stages would not fit beside it
+  // words of a team's table; halved for teams of four and two, whose stream then starts
+  // after one round of loads (64 x 2048 selected from an E4M3 cache 56 us, else 61)
   static constexpr int kTabWords = (W == 2 || W == 4 ? kTab / 2 : kTab) / kTeams;
-  // a warp's ring: 12 KB, or 24 with one CTA an SM, or what the teams' query rows leave
-  static constexpr int kMost = kOcc == 2 ? 12288 : 24576;
+  // a warp's ring: 12 KB, of a small team 8 (16 rows, 64 x 2048 selected 94 us, with
+  // 12 KB 104; 8 rows 87 and 89; 64 contexts of 100 - 500 15.4 and 16.1), with one CTA
+  // an SM twice that, or what the teams' query rows leave
+  static constexpr int kMost = (W == kWarps ? 12288 : 8192) * (kOcc == 2 ? 1 : 2);
   static constexpr int kRoom = (222 * 1024 / kOcc - kTeams * (kQBytes + kTabWords * 4)) / kWarps;
   static constexpr int kStages = (kRoom < kMost ? kRoom : kMost) / kHalf;
   static constexpr int kRing = kStages * kHalf;

@@ -111,29 +111,31 @@ int common_shift(int64_t x, int64_t y) {
 
 // Warps that share an item: 8 (a CTA), 4, 2 or 1, or 0: items split over all CTAs
 // and joined.  By an estimate of the call's microseconds for `items` items of up
-// to `bytes` bytes of cache: 5 to start; 2 to set an item up; 7.1 TB/s in all and
-// what a warp's ring and products let it stream, 6.2 GB/s, 12.4 where one CTA an
-// SM has rings twice as long, 5.2 with sixteen rows, 5 with 32; 15 to start, cut
-// and join.  Selected positions are as many for every item, and a last wave of few
-// items costs its whole time.  Contexts are taken to fill half of their room on
-// average, and the longest, which may come last, costs 0.4 of its time.  Over 256
-// measured cases of types, head layouts and lengths this choice takes 1.5 % more
-// time than the best of the five, and 12 % less than splitting all but the short
-// ones.
+// to `bytes` bytes of cache: 5 to start; 2.5 to set an item up; 7.1 TB/s in all and
+// what a warp's ring and products let it stream: 6.2 GB/s, 5.2 with 16 rows, 5 with
+// 32; 12.4, 7.8 and 7 where one CTA an SM leaves more room; of E4M3 codes 0.7 of
+// that; 15 to start, cut and join.  Selected positions are as many for every item,
+// and a last wave of few items costs its whole time.  Contexts are taken to fill
+// half of their room on average, and the longest, which may come last, costs 0.4 of
+// its time.  Over 456 measured cases of types, head layouts and lengths this choice
+// takes 1.2 % more time than the best of the five, and 12 % less than splitting all
+// but the short ones.
 //   us (8 heads, 8 rows of 128, bf16)     split   8 warps   4     2     1
-//   64 x 2048 selected                      94      88      89    98   177
-//   80 x 2048 selected                     113     121     144   119   180
-//   64 x 512 selected                       33      30      27    29    50
+//   64 x 2048 selected                      94      88      87   106   177
+//   80 x 2048 selected                     113     122     143   122   180
+//   64 x 512 selected                       33      30      26    31    50
 //   128 x 128 selected                      23      23      16    13    16
-//   304 x 512 selected                     116     115     110   105   101
+//   304 x 512 selected                     115     115     111   104   101
 //   128 contexts of 64 - 512                38      34      33    33    45
-//   128 of 128 - 1024                       58      52      56    59    81
-//   64 of 256 - 2048                        54      53      57    74   142
-//   256 of 2048                            308     297     304   300   309
-//   8 of 8192 - 32768                      103     203     517  1032  2130
-int attn_team(int64_t items, double bytes, bool listed, int ctas, int occ, int nt) {
-  const double setup = 2.0;
-  const double warp_rate = nt == 4 ? 5.0e3 : (nt == 2 ? 5.2e3 : 6.2e3) * (occ == 2 ? 1.0 : nt == 2 ? 1.5 : 2.0);
+//   128 of 128 - 1024                       57      52      56    58    81
+//   64 of 256 - 2048                        55      53      56    78   142
+//   256 of 2048                            308     297     305   297   309
+//   8 of 8192 - 32768                      103     203     532  1054  2130
+int attn_team(int64_t items, double bytes, bool listed, int ctas, int occ, int nt, bool f8) {
+  const double setup = 2.5;
+  const double ring = nt == 4 ? (occ == 2 ? 5.0e3 : 7.0e3)
+                      : nt == 2 ? (occ == 2 ? 5.2e3 : 7.8e3) : (occ == 2 ? 6.2e3 : 12.4e3);
+  const double warp_rate = f8 ? 0.7 * ring : ring;
   const double rate = fmin(7.1e6, ctas * 8 * warp_rate);
   const double all = (double)items * bytes / rate * (listed ? 1.0 : 0.5);
   double best = 15.0 + setup * (double)items / ctas + all;
@@ -473,7 +475,8 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   const int occ = idx::attn_occupancy(D, kv->dtype, nt);
   int64_t ctas = (int64_t)sms * occ;
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
-  const int team = attn_team(items, (double)keys * D * 2 * elt, topk_idx != nullptr, (int)ctas, occ, nt);
+  const int team = attn_team(items, (double)keys * D * 2 * elt, topk_idx != nullptr, (int)ctas, occ, nt,
+                             kv->dtype == IDX_E4M3);
   a.split = units > 2 && team == 0;
   a.team = team == 0 ? 8 : team;
   const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : (items * a.team + 7) / 8;
