@@ -44,9 +44,9 @@
 //
 // Measured (one call, new inputs in turn): 64 requests of 8K - 32K keys, 32/8
 // heads of 128, bf16, 5.2 GB: 724 us, 7.19 TB/s; 64 x 2048 selected positions
-// (0.54 GB) 94 us, 5.7 TB/s, of which about 10 us are the start of the stream
-// and the join and 8 the spread of the CTAs' ends.  The tensor pipe is 13 - 15 %
-// busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
+// (0.54 GB) 87 us, 6.2 TB/s, items whole by four warps each (split and joined
+// 94).  Rows gathered one by one take 0.91 of the copy rate at 256 bytes, 0.96 at
+// 512, 0.70 at 128.  The tensor pipe is 13 - 15 % busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
 // from 32 rows over an E4M3 cache on (0.53 of the copy rate).
 #pragma once
 
