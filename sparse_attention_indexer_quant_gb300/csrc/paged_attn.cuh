@@ -3,9 +3,8 @@
 // Work.  An item is one kv head of one request with its query rows (next_n
 // tokens times the heads of the group; with a selection, one token's group),
 // up to 8 * NT of them.  An item is taken whole by a team of W = 8, 4, 2 or 1
-// warps of a CTA, the blocks' order left to the hardware: long items by whole
-// CTAs, short ones by few warps, so that one team sets an item up while others
-// stream.  Where that would leave SMs idle (few or long items; the caller
+// warps, their order left to the hardware: long items by eight warps, short ones by
+// few, so that some teams of an SM set items up while others stream.  Where that would leave SMs idle (few or long items; the caller
 // estimates both) the items are split: their keys are cut into units of 8 * KS
 // (64 KB of cache for most shapes), numbered item by item over the whole batch,
 // and the units into segments (see Cut).  With R resident CTAs the first R segments take
@@ -62,7 +61,6 @@ namespace idx {
 namespace attn {
 
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTab = 2048;  // words of the table of resolved page groups / listed positions
 constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -77,8 +75,12 @@ constexpr float kLift = MB ? 0.f : 7.f;
 template <int D, int CT>
 constexpr int row_bytes() { return D * (CT == IDX_E4M3 ? 1 : 2); }
 
-// W warps (a team) share an item; a CTA has eight warps.
-template <int D, int CT, int NT, int W>
+// W warps (a team) share an item.  A CTA is one team; where rows of at most 128
+// bytes are gathered one by one, it is eight warps, teams of neighbouring heads,
+// whose rows lie close together: 64 x 2048 selected from an E4M3 cache 57 us, as
+// CTAs of four warps 63 (of 256-byte rows 86 and 85; contexts: 128 of 100 - 250 keys
+// 16.7 and 14.9).
+template <int D, int CT, int NT, bool listed, int W>
 struct Cfg {
   static_assert(W == kWarps || W == 4 || W == 2 || W == 1, "");
   static constexpr bool kF8 = CT == IDX_E4M3;
@@ -94,22 +96,24 @@ struct Cfg {
   static constexpr int kOcc = attn_occupancy(D, CT, NT);
   static constexpr int kPitch = W < kWarps ? D : D + 4;  // floats of a row of the merge buffer
   static constexpr int kSums = kRows * kPitch * 4;
-  static constexpr int kTeams = kWarps / W;
+  static constexpr int kTeams = listed && kRowB <= 128 ? kWarps / W : 1;
+  static constexpr int kThreads = 32 * W * kTeams;
+  static constexpr int kCtas = kOcc * (kWarps / (W * kTeams));  // resident per SM
   static constexpr int kQBytes = kRows * D * 2;
-  // words of a team's table; halved for teams of four and two, whose stream then starts
+  // words of a team's table; halved for four and two warps, whose stream then starts
   // after one round of loads (64 x 2048 selected from an E4M3 cache 56 us, else 61)
-  static constexpr int kTabWords = (W == 2 || W == 4 ? kTab / 2 : kTab) / kTeams;
-  // a warp's ring: 12 KB, of a small team 8 (16 rows, 64 x 2048 selected 94 us, with
+  static constexpr int kTabWords = (W == 2 || W == 4 ? kTab / 2 : kTab) * W / kWarps;
+  // a warp's ring: 12 KB, of a small CTA 8 (16 rows, 64 x 2048 selected 94 us, with
   // 12 KB 104; 8 rows 87 and 89; 64 contexts of 100 - 500 15.4 and 16.1), with one CTA
-  // an SM twice that, or what the teams' query rows leave
+  // an SM twice that, or what the query rows leave
   static constexpr int kMost = (W == kWarps ? 12288 : 8192) * (kOcc == 2 ? 1 : 2);
-  static constexpr int kRoom = (222 * 1024 / kOcc - kTeams * (kQBytes + kTabWords * 4)) / kWarps;
+  static constexpr int kRoom = (222 * 1024 / kCtas / kTeams - kQBytes - kTabWords * 4) / W;
   static constexpr int kStages = (kRoom < kMost ? kRoom : kMost) / kHalf;
   static constexpr int kRing = kStages * kHalf;
-  static constexpr int kSmem = kWarps * kRing + kTeams * (kQBytes + kTabWords * 4);
+  static constexpr int kSmem = kTeams * (W * kRing + kQBytes + kTabWords * 4);
   static_assert(kSums <= kRing, "a warp's sums fit its ring");
   static_assert(kStages >= 2 && kRing % kHalf == 0, "");
-  static_assert(kSmem * kOcc <= 222 * 1024, "");
+  static_assert(kSmem * kCtas <= 222 * 1024, "");
 };
 
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
@@ -699,34 +703,36 @@ struct TileOf<D, CT, 1, KS> {
 };
 
 template <int D, int CT, int NT, bool listed, int W>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, CT, NT, W>::kOcc))
+__global__ void __launch_bounds__((Cfg<D, CT, NT, listed, W>::kThreads), (Cfg<D, CT, NT, listed, W>::kCtas))
 paged_attn_kernel(const __grid_constant__ AttnArgs a) {
-  using C = Cfg<D, CT, NT, W>;
+  using C = Cfg<D, CT, NT, listed, W>;
   constexpr bool F8 = C::kF8, MB = C::kMmaBf16;
   constexpr int KS = C::kKS, ROWB = C::kRowB, NS = C::kStages;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ int s_warp[kWarps], s_pieces[kWarps][4], s_last[kWarps];
+  __shared__ int s_warp[W], s_pieces[W][4], s_lasts[C::kTeams][W];
   __shared__ int s_base, s_req, s_seg;
   // log2 score per product (with a cap: its argument), and ones for capped scores
   __shared__ __align__(8) float s_mults[C::kTeams][C::kRows], s_one[C::kRows];
   __shared__ int s_ends[C::kTeams][C::kRows];  // first key past a row's sight
-  __shared__ float2 s_ml[kWarps][C::kRows];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the team that shares an item, and this thread's place in it
+  __shared__ float2 s_mls[C::kTeams][W][C::kRows];
   constexpr int TT = 32 * W;
-  const int team = warp / W, tw = warp % W, tid = (int)threadIdx.x % TT;
+  // the team, and this thread's and warp's place in it
+  const int team = (int)threadIdx.x / TT, tid = (int)threadIdx.x % TT, lane = tid & 31, warp = tid >> 5;
   auto sync = [&]() {
     if (W == 1) __syncwarp();
-    else if (W == kWarps) __syncthreads();
+    else if (C::kTeams == 1) __syncthreads();
     else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TT) : "memory");
   };
   float* s_mult = s_mults[team];
   int* s_end = s_ends[team];
-  uint8_t* ring = smem + warp * C::kRing;
+  int* s_last = s_lasts[team];
+  float2(*s_ml)[C::kRows] = s_mls[team];
+  uint8_t* rings = smem + team * (W * C::kRing);
+  uint8_t* ring = rings + warp * C::kRing;
   const uint32_t ring_u = smem_u32(ring);
-  uint8_t* q_sm = smem + kWarps * C::kRing + team * C::kQBytes;
+  uint8_t* q_sm = smem + C::kTeams * (W * C::kRing) + team * C::kQBytes;
   const uint32_t q_u = smem_u32(q_sm);
-  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + kWarps * C::kRing + C::kTeams * C::kQBytes) +
+  uint32_t* tab = reinterpret_cast<uint32_t*>(smem + C::kTeams * (W * C::kRing + C::kQBytes)) +
                   team * C::kTabWords;
   // offsets into k and v: one table where both have the same strides
   uint32_t* vtab = a.one_table ? tab : tab + C::kTabWords / 2;
@@ -756,12 +762,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       U = reqs * HR * (list_units + kSetup);
     } else {
       int sum = 0;
-      for (int b = tid; b < reqs; b += kThreads) sum += span_of(b).units + kSetup;
+      for (int b = tid; b < reqs; b += TT) sum += span_of(b).units + kSetup;
       sum = warp_incl_sum(sum, lane);
       if (lane == 31) s_warp[warp] = sum;
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) U += s_warp[w];
+      for (int w = 0; w < W; ++w) U += s_warp[w];
       U *= HR;
     }
   }
@@ -776,7 +782,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) pieces[j] = reqs * ((list_units + q0 + j * step - 1) / (q0 + j * step));
     } else {
-      for (int b = tid; b < reqs; b += kThreads) {
+      for (int b = tid; b < reqs; b += TT) {
         const int units = span_of(b).units;
 #pragma unroll
         for (int j = 0; j < 4; ++j) pieces[j] += (units + q0 + j * step - 1) / (q0 + j * step);
@@ -791,7 +797,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       for (int j = 0; j < 4; ++j) {
         pieces[j] = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) pieces[j] += s_pieces[w][j];
+        for (int w = 0; w < W; ++w) pieces[j] += s_pieces[w][j];
       }
     }
 #pragma unroll
@@ -810,12 +816,12 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   // The last thread, which has the least to do when sums are joined, fetches the
   // CTA's next segment.
   auto claim = [&]() {
-    if (split && cut.K > 0 && tid == kThreads - 1) {
+    if (split && cut.K > 0 && tid == TT - 1) {
       const uint32_t t = claim_item(a.counter, a.gen, a.errors);
       s_seg = t >= (uint32_t)(cut.segments() - cut.R) ? cut.segments() : cut.R + (int)t;
     }
   };
-  for (int seg = W < kWarps ? blockIdx.x * C::kTeams + team : blockIdx.x; seg < segments;) {
+  for (int seg = blockIdx.x * C::kTeams + team; seg < segments;) {
     // ---- the segment's units [u0, u1), and the request its first unit belongs to
     int u0, u1, base, req;  // base: first unit of request `req`
     if (!split) {  // one team per item; units are counted from its request's first
@@ -834,7 +840,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       } else {
         int before = 0;  // weights of the requests before these
         if (tid == 0) s_req = -1;
-        for (int b0 = 0; b0 < reqs; b0 += kThreads) {
+        for (int b0 = 0; b0 < reqs; b0 += TT) {
           const int b = b0 + tid;
           const int mine = b < reqs ? weight(span_of(b).units) : 0;
           int incl = warp_incl_sum(mine, lane);
@@ -843,7 +849,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           __syncthreads();
           int total = 0;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
+          for (int w = 0; w < W; ++w) {
             if (w < warp) incl += s_warp[w];
             total += s_warp[w];
           }
@@ -1051,7 +1057,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         sync();
         if (listed) {
 #pragma unroll
-          for (int w = 0; w < W; ++w) last = max(last, s_last[team * W + w]);
+          for (int w = 0; w < W; ++w) last = max(last, s_last[w]);
           sb = min(sb, sa + last / C::kUnit + (last < 0 ? 0 : 1));
         }
 
@@ -1069,7 +1075,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             const uint32_t dst = ring_u + put * C::kHalf;
             src0 += cl * 16;
             if (listed) {
-              const uint32_t* e0 = tb_ + t * C::kUnit + tw * KS + rl;
+              const uint32_t* e0 = tb_ + t * C::kUnit + warp * KS + rl;
 #pragma unroll
               for (int j = 0; j < KS / RPI; ++j) {
                 const uint32_t e = e0[j * RPI];
@@ -1081,7 +1087,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
               const int64_t ts = is_v ? v_ts : k_ts;
 #pragma unroll
               for (int gr = 0; gr < KS / 16; ++gr) {
-                const int grp = t * (C::kUnit / 16) + tw * (KS / 16) + gr;
+                const int grp = t * (C::kUnit / 16) + warp * (KS / 16) + gr;
                 const uint32_t e = tb_[grp];
                 const int key = (sp.t0 + sa) * C::kUnit + grp * 16 + rl;
                 const uint8_t* src = src0 + (e != kNone ? (uint64_t)e * a.off_unit + rl * ts : 0);
@@ -1119,7 +1125,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           get = get + 1 == NS ? 0 : get + 1;
           issue(2 * t + NS);
 
-          const int tile0 = t * C::kUnit + tw * KS;  // within the sub-range
+          const int tile0 = t * C::kUnit + warp * KS;  // within the sub-range
           const int key0 = (sp.t0 + sa) * C::kUnit + tile0;
           bool whole;  // every key of the tile is seen by every row
           if (listed) {
@@ -1167,15 +1173,15 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         const int r = i / QPR, d = (i % QPR) * 4;
         float mx = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[team * W + w][r].x);
+        for (int w = 0; w < W; ++w) mx = fmaxf(mx, s_ml[w][r].x);
         float lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-          const float2 ml = s_ml[team * W + w][r];
+          const float2 ml = s_ml[w][r];
           if (ml.x == -INFINITY && ml.y == 0.f) continue;  // the warp saw nothing of this row
           const float f = ml.x == -INFINITY ? 1.f : ex2(ml.x - mx);
-          const float4 x = *reinterpret_cast<const float4*>(smem + (team * W + w) * C::kRing + (r * C::kPitch + d) * 4);
+          const float4 x = *reinterpret_cast<const float4*>(rings + w * C::kRing + (r * C::kPitch + d) * 4);
           lsum += ml.y * f;
           acc.x += x.x * f;
           acc.y += x.y * f;
@@ -1217,18 +1223,24 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   }
 }
 
-template <int D, int CT, int NT, int W>
-cudaError_t launch_team(const AttnArgs& a, cudaStream_t stream) {
-  using C = Cfg<D, CT, NT, W>;
-  auto kern = a.topk_idx ? paged_attn_kernel<D, CT, NT, true, W> : paged_attn_kernel<D, CT, NT, false, W>;
+template <int D, int CT, int NT, bool listed, int W>
+cudaError_t launch_items(const AttnArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, CT, NT, listed, W>;
+  auto kern = paged_attn_kernel<D, CT, NT, listed, W>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, dim3(a.grid), dim3(kThreads), C::kSmem, stream, a);
+  return launch_dependent(kern, dim3((a.grid + C::kTeams - 1) / C::kTeams), dim3(C::kThreads), C::kSmem,
+                          stream, a);
+}
+
+template <int D, int CT, int NT, int W>
+cudaError_t launch_team(const AttnArgs& a, cudaStream_t stream) {
+  return a.topk_idx ? launch_items<D, CT, NT, true, W>(a, stream) : launch_items<D, CT, NT, false, W>(a, stream);
 }
 
 template <int D, int CT, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
-  switch (a.team) {
+  switch (a.warps) {
     case 1: return launch_team<D, CT, NT, 1>(a, stream);
     case 2: return launch_team<D, CT, NT, 2>(a, stream);
     case 4: return launch_team<D, CT, NT, 4>(a, stream);

@@ -107,8 +107,8 @@ struct AttnArgs {
   int32_t one_table;  // k and v have the same page and token strides
   int32_t q_bf16;     // type of q and out
   int32_t split;      // 0: items whole, no join
-  int32_t team;       // warps that share an item: 8, 4, 2 or 1 (fewer than 8 only with split = 0)
-  int32_t grid;
+  int32_t warps;      // warps that share an item: 8, 4, 2 or 1 (fewer than 8 only with split = 0)
+  int32_t grid;       // teams
   idx_device_errors* errors;
 };
 // Tiles of eight query rows an item of `rows` rows takes: 1, 2 or 4 (head_dim

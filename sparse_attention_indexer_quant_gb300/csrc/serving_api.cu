@@ -131,7 +131,7 @@ int common_shift(int64_t x, int64_t y) {
 //   64 of 256 - 2048                        55      53      56    78   142
 //   256 of 2048                            308     297     305   297   309
 //   8 of 8192 - 32768                      103     203     532  1054  2130
-int attn_team(int64_t items, double bytes, bool listed, int ctas, int occ, int nt, bool f8) {
+int attn_warps(int64_t items, double bytes, bool listed, int ctas, int occ, int nt, bool f8) {
   const double setup = 2.5;
   const double ring = nt == 4 ? (occ == 2 ? 5.0e3 : 7.0e3)
                       : nt == 2 ? (occ == 2 ? 5.2e3 : 7.8e3) : (occ == 2 ? 6.2e3 : 12.4e3);
@@ -139,7 +139,7 @@ int attn_team(int64_t items, double bytes, bool listed, int ctas, int occ, int n
   const double rate = fmin(7.1e6, ctas * 8 * warp_rate);
   const double all = (double)items * bytes / rate * (listed ? 1.0 : 0.5);
   double best = 15.0 + setup * (double)items / ctas + all;
-  int team = 0;
+  int warps = 0;
   for (int w = 8; w >= 1; w /= 2) {
     const int64_t slots = (int64_t)ctas * (8 / w);
     const double alone = bytes / (w * warp_rate);
@@ -154,10 +154,10 @@ int attn_team(int64_t items, double bytes, bool listed, int ctas, int occ, int n
     }
     if (t < best) {
       best = t;
-      team = w;
+      warps = w;
     }
   }
-  return team;
+  return warps;
 }
 
 bool attn_shape_ok(int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D) {
@@ -475,11 +475,11 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   const int occ = idx::attn_occupancy(D, kv->dtype, nt);
   int64_t ctas = (int64_t)sms * occ;
   if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
-  const int team = attn_team(items, (double)keys * D * 2 * elt, topk_idx != nullptr, (int)ctas, occ, nt,
-                             kv->dtype == IDX_E4M3);
-  a.split = units > 2 && team == 0;
-  a.team = team == 0 ? 8 : team;
-  const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : (items * a.team + 7) / 8;
+  const int warps = attn_warps(items, (double)keys * D * 2 * elt, topk_idx != nullptr, (int)ctas, occ, nt,
+                               kv->dtype == IDX_E4M3);
+  a.split = units > 2 && warps == 0;
+  a.warps = warps == 0 ? 8 : warps;
+  const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
   if ((units + 64) * items > INT32_MAX || items * a.part_rows > INT32_MAX)
     return fail(IDX_ERR_INVALID_ARG, "%lld query row tiles of up to %lld keys: too much for one call",
                 (long long)items, (long long)keys);
