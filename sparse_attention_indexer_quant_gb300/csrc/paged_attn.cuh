@@ -76,10 +76,11 @@ template <int D, int CT>
 constexpr int row_bytes() { return D * (CT == IDX_E4M3 ? 1 : 2); }
 
 // W warps (a team) share an item.  A CTA is one team; where rows of at most 128
-// bytes are gathered one by one, it is eight warps, teams of neighbouring heads,
-// whose rows lie close together: 64 x 2048 selected from an E4M3 cache 57 us, as
-// CTAs of four warps 63 (of 256-byte rows 86 and 85; contexts: 128 of 100 - 250 keys
-// 16.7 and 14.9).
+// bytes are gathered one by one and a team is less than eight warps, it is all the
+// teams of an SM, of neighbouring heads, whose rows lie close together: 64 x 2048
+// selected from an E4M3 cache 56 us, as CTAs of one team 66; of head_dim 64 53 and
+// 63 (rows of 256 bytes 87 and 86; contexts, whose lengths differ, gain by single
+// teams: 128 of 100 - 250 keys 14.9, two teams a CTA 16.7).
 template <int D, int CT, int NT, bool listed, int W>
 struct Cfg {
   static_assert(W == kWarps || W == 4 || W == 2 || W == 1, "");
@@ -96,9 +97,9 @@ struct Cfg {
   static constexpr int kOcc = attn_occupancy(D, CT, NT);
   static constexpr int kPitch = W < kWarps ? D : D + 4;  // floats of a row of the merge buffer
   static constexpr int kSums = kRows * kPitch * 4;
-  static constexpr int kTeams = listed && kRowB <= 128 ? kWarps / W : 1;
+  static constexpr int kTeams = listed && kRowB <= 128 && W < kWarps ? kOcc * kWarps / W : 1;
   static constexpr int kThreads = 32 * W * kTeams;
-  static constexpr int kCtas = kOcc * (kWarps / (W * kTeams));  // resident per SM
+  static constexpr int kCtas = kOcc * kWarps / (W * kTeams);  // resident per SM
   static constexpr int kQBytes = kRows * D * 2;
   // words of a team's table; halved for four and two warps, whose stream then starts
   // after one round of loads (64 x 2048 selected from an E4M3 cache 56 us, else 61)
