@@ -43,9 +43,9 @@
 //
 // Measured (one call, new inputs in turn): 64 requests of 8K - 32K keys, 32/8
 // heads of 128, bf16, 5.2 GB: 724 us, 7.19 TB/s; 64 x 2048 selected positions
-// (0.54 GB) 87 us, 6.2 TB/s, items whole by four warps each (split and joined
-// 94).  Rows gathered one by one take 0.91 of the copy rate at 256 bytes, 0.96 at
-// 512, 0.70 at 128.  The tensor pipe is 13 - 15 % busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
+// (0.54 GB) 86 us, 6.3 TB/s, items whole by four warps each (split and joined
+// 94).  Rows gathered one by one take 0.92 of the copy rate at 256 bytes, 0.95 at
+// 512, 0.70 - 0.74 at 128.  The tensor pipe is 13 - 15 % busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
 // from 32 rows over an E4M3 cache on (0.53 of the copy rate).
 #pragma once
 
@@ -104,7 +104,7 @@ struct Cfg {
   // words of a team's table; halved for four and two warps, whose stream then starts
   // after one round of loads (64 x 2048 selected from an E4M3 cache 56 us, else 61)
   static constexpr int kTabWords = (W == 2 || W == 4 ? kTab / 2 : kTab) * W / kWarps;
-  // a warp's ring: 12 KB, of a small CTA 8 (16 rows, 64 x 2048 selected 94 us, with
+  // a warp's ring: 12 KB, of a small team 8 (16 rows, 64 x 2048 selected 94 us, with
   // 12 KB 104; 8 rows 87 and 89; 64 contexts of 100 - 500 15.4 and 16.1), with one CTA
   // an SM twice that, or what the query rows leave
   static constexpr int kMost = (W == kWarps ? 12288 : 8192) * (kOcc == 2 ? 1 : 2);

@@ -117,20 +117,20 @@ int common_shift(int64_t x, int64_t y) {
 // that; 15 to start, cut and join.  Selected positions are as many for every item,
 // and a last wave of few items costs its whole time.  Contexts are taken to fill
 // half of their room on average, and the longest, which may come last, costs 0.4 of
-// its time.  Over 456 measured cases of types, head layouts and lengths this choice
-// takes 1.2 % more time than the best of the five, and 12 % less than splitting all
-// but the short ones.
+// its time.  Over 277 measured cases of types, head layouts and lengths this choice
+// takes 1.7 % more time than the best of the five on average (26 % at most) and
+// 13 % less than splitting always (14 % more at most).
 //   us (8 heads, 8 rows of 128, bf16)     split   8 warps   4     2     1
-//   64 x 2048 selected                      94      88      87   106   177
-//   80 x 2048 selected                     113     122     143   122   180
-//   64 x 512 selected                       33      30      26    31    50
-//   128 x 128 selected                      23      23      16    13    16
-//   304 x 512 selected                     115     115     111   104   101
-//   128 contexts of 64 - 512                38      34      33    33    45
-//   128 of 128 - 1024                       57      52      56    58    81
-//   64 of 256 - 2048                        55      53      56    78   142
-//   256 of 2048                            308     297     305   297   309
-//   8 of 8192 - 32768                      103     203     532  1054  2130
+//   64 x 2048 selected                      94      88      86   100   153
+//   80 x 2048 selected                     113     120     135   116   162
+//   64 x 512 selected                       33      30      26    30    44
+//   128 x 128 selected                      23      23      15    13    15
+//   304 x 512 selected                     114     114     107   103   104
+//   128 contexts of 64 - 512                38      35      31    31    38
+//   128 of 128 - 1024                       57      52      53    54    68
+//   64 of 256 - 2048                        54      53      52    66   109
+//   256 of 2048                            307     297     299   295   310
+//   8 of 8192 - 32768                      103     203     413   788  1554
 int attn_warps(int64_t items, double bytes, bool listed, int ctas, int occ, int nt, bool f8) {
   const double setup = 2.5;
   const double ring = nt == 4 ? (occ == 2 ? 5.0e3 : 7.0e3)
