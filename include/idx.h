@@ -433,7 +433,9 @@ typedef struct {
  *   pool_head    [1] int32: entries of free_pages taken so far;
  *   pool_head_out [1] int32 out: the same after this step (another word than
  *                pool_head, which other blocks of the launch may still read).
- *   context_lens [B] int32 out: cached + new.
+ *   context_lens [B] int32 out: cached + new; may be cached_lens itself, whose
+ *                lengths then advance in place, and one block makes the whole
+ *                plan (64K tokens take 195 us, apart 4.7).
  *   query_start  [B+1] int32 out: exclusive sums of new_lens.
  *   slot_mapping [num_tokens] int64, positions [num_tokens] int32, token_seq
  *                [num_tokens] int32 out: for the step's tokens, request by
@@ -445,6 +447,8 @@ typedef struct {
  * from the list or outside [0, num_blocks) (block table entry -1, its tokens
  * slot -1), a token whose existing page id is outside the cache (slot -1), and
  * every token past num_tokens (not written).
+ * Refused: an array that is written and overlaps another one, context_lens =
+ * cached_lens apart.
  *   page_size 16, 32, 64 or 128; num_free may be 0.
  * ------------------------------------------------------------------------ */
 IDX_API idx_status idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int32_t B,

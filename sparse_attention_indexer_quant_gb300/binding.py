@@ -492,7 +492,9 @@ def plan_step(cached_lens, new_lens, block_table, free_pages, pool_head, num_tok
     [B], query_start [B+1], slot_mapping [num_tokens] (int64), positions and
     token_seq [num_tokens], and the advanced pool_head [1] (all int32 but the
     slots); num_tokens may exceed the step's tokens (slot -1, position 0 and
-    request -1 past them).  `out`: an earlier plan to write into."""
+    request -1 past them).  `out`: an earlier plan to write into; its
+    context_lens may be cached_lens (advanced in place), other arrays must not
+    overlap."""
     return StepPlan(*_call(_serving.plan_step, stream, cached_lens, new_lens, block_table,
                            free_pages, pool_head, num_tokens, num_blocks, page_size, out, errors))
 

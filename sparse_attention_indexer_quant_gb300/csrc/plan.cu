@@ -66,13 +66,19 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(PlanArgs a) {
     const int nb = min(kChunk, a.B - b0);
     const bool mine = chunk % (int)gridDim.x == (int)blockIdx.x;
     long long tok[kPerThread], pages[kPerThread], st = 0, sp = 0;
+    int lens[kPerThread], adds[kPerThread];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const int r = tid * kPerThread + i;
-      int cached = 0, fresh = 0;
+      // not through the read-only path: context_lens may be this array
+      lens[i] = r < nb ? a.cached[b0 + r] : 0;
+      adds[i] = r < nb ? __ldg(a.fresh + b0 + r) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int r = tid * kPerThread + i;
+      int cached = lens[i], fresh = adds[i];
       if (r < nb) {
-        cached = __ldg(a.cached + b0 + r);
-        fresh = __ldg(a.fresh + b0 + r);
         if (cached < 0 || fresh < 0) {
           if (mine) ++bad;
           cached = fresh = 0;
@@ -185,8 +191,10 @@ __global__ void __launch_bounds__(kThreads) plan_step_kernel(PlanArgs a) {
 }  // namespace
 
 cudaError_t launch_plan_step(const PlanArgs& a, int sms, cudaStream_t stream) {
-  // one block per 256 tokens (a request's pages follow its tokens), at most one per SM
-  const int64_t want = (a.num_tokens + kThreads - 1) / kThreads;
+  // One block per 256 tokens (a request's pages follow its tokens), at most one per
+  // SM.  Where the lengths are advanced in place, one block in all: every block sums
+  // all lengths, and here they change as it goes (each by the thread that has read it).
+  const int64_t want = a.context_lens == a.cached ? 1 : (a.num_tokens + kThreads - 1) / kThreads;
   const int grid = (int)(want < 1 ? 1 : (want > sms ? sms : want));
   return launch_dependent(plan_step_kernel, dim3(grid), dim3(kThreads), 0, stream, a);
 }

@@ -31,6 +31,17 @@ int page_shift_of(int32_t page_size) {
   return -1;
 }
 
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+bool overlap(const Range& a, const Range& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.p && b.p && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes &&
+         y < x + (uintptr_t)a.bytes;
+}
+
 bool stride_ok(int64_t stride, int elt) {
   return stride >= 0 && stride <= (int64_t)1 << 48 && (stride * elt) % 16 == 0;
 }
@@ -188,6 +199,27 @@ idx_status idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, in
     return fail(IDX_ERR_INVALID_ARG, "num_blocks=%lld", (long long)num_blocks);
   if (num_tokens < 0 || num_tokens > (int64_t)INT32_MAX)
     return fail(IDX_ERR_INVALID_ARG, "num_tokens=%lld", (long long)num_tokens);
+  // Every block reads all inputs while others write: an array that is written overlaps
+  // no other one, but for context_lens = cached_lens (then one block does it all).
+  const Range written[7] = {{context_lens, 4ll * B, "context_lens"},
+                            {query_start, 4ll * B + 4, "query_start"},
+                            {slot_mapping, 8 * num_tokens, "slot_mapping"},
+                            {positions, 4 * num_tokens, "positions"},
+                            {token_seq, 4 * num_tokens, "token_seq"},
+                            {pool_head_out, 4, "pool_head_out"},
+                            {block_table, 4ll * B * max_blocks, "block_table"}};
+  const Range read[4] = {{cached_lens, 4ll * B, "cached_lens"},
+                         {new_lens, 4ll * B, "new_lens"},
+                         {free_pages, 4ll * num_free, "free_pages"},
+                         {pool_head, 4, "pool_head"}};
+  for (int i = 0; i < 7; ++i) {
+    for (const Range& r : read)
+      if (overlap(written[i], r) && !(i == 0 && &r == read && context_lens == cached_lens))
+        return fail(IDX_ERR_INVALID_ARG, "%s overlaps %s", written[i].name, r.name);
+    for (int j = 0; j < i; ++j)
+      if (overlap(written[i], written[j]))
+        return fail(IDX_ERR_INVALID_ARG, "%s overlaps %s", written[i].name, written[j].name);
+  }
   int sms = 0;
   idx_status s = idx::current_device_ok(&sms);
   if (s != IDX_OK) return s;
@@ -196,8 +228,6 @@ idx_status idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, in
       (num_free > 0 && !free_pages) ||
       (num_tokens > 0 && (!slot_mapping || !positions || !token_seq)))
     return fail(IDX_ERR_INVALID_ARG, "null pointer argument");
-  if (pool_head == pool_head_out)
-    return fail(IDX_ERR_INVALID_ARG, "pool_head_out must be another word than pool_head");
   if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(block_table, 4) ||
       !aligned(free_pages, 4) || !aligned(pool_head, 4) || !aligned(pool_head_out, 4) ||
       !aligned(context_lens, 4) || !aligned(query_start, 4) || !aligned(slot_mapping, 8) ||
