@@ -545,7 +545,8 @@ IDX_API idx_status idx_qk_norm_rope_insert(
  *              A row that sees nothing gets zeros and -inf.
  *   workspace  at least idx_paged_attention_workspace_bytes(...) bytes, 256-byte
  *              aligned, no initialisation; calls that share it must not overlap.
- * Scores, softmax statistics and sums are fp32; the weights enter the second
+ * Scores, softmax statistics and sums are fp32 (a cap of any size adds at most
+ * 2^-20 of the capped score); the weights enter the second
  * product as two 16-bit terms (over an fp16 or E4M3 cache weights below 2^-32 of
  * a row's highest count as zero; an infinite value in sight gives NaN).  Results do not depend on the order in which
  * blocks run.  Over-long contexts (clamped), negative ones (0) and page ids

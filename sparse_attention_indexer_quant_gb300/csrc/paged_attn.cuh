@@ -172,11 +172,27 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// A capped score in log2 units: c log2(e) tanh(y) with tanh(y) = 1 - 2 / (1 + e^2y),
-// off by at most 2^-21 c (the exponential's and the reciprocal's 2^-22 each).
-// With the library's tanhf the ragged capped case took 25.0 us instead of 24.0.
-__device__ __forceinline__ float capped(float y, float c_log2e) {
-  return fmaf(-2.f * c_log2e, __fdividef(1.f, 1.f + ex2(2.f * kLog2e * y)), c_log2e);
+// A capped score: c tanh(x / c) for x and the cap c in log2 units, inv = 1 / c.
+// Below half a cap tanh(y) = y P(y^2), P the interpolant of tanh(y) / y at Chebyshev
+// nodes (off by 2^-24), so that the score's error is relative to the score however
+// large the cap is (a cap past every score changes nothing); above, tanh(y) =
+// 1 - 2 / (1 + e^2y) with the exponential's and the reciprocal's 2^-22.  In all
+// at most 2^-20 of the score.  The second form alone is off by 2^-21 of the cap.
+// A tile whose scores are all below takes the first form alone (ragged capped case
+// 21.0 us, both forms and a choice for every score 22.8, the second alone 20.4).
+constexpr float kCapNear = 0.5f;
+__device__ __forceinline__ float capped_near(float x, float inv) {
+  const float y = x * inv, z = y * y;
+  float p = 1.798874440e-02f;
+  p = fmaf(p, z, -5.338711063e-02f);
+  p = fmaf(p, z, 1.333047649e-01f);
+  p = fmaf(p, z, -3.333331108e-01f);
+  return x * fmaf(p, z, 1.f);
+}
+__device__ __forceinline__ float capped(float x, float c, float inv) {
+  const float y = x * inv;
+  const float far = fmaf(__fdividef(-2.f, 1.f + ex2(2.f * kLog2e * fabsf(y))), c, c);
+  return fabsf(y) < kCapNear ? capped_near(x, inv) : copysignf(far, y);
 }
 
 // Shared-memory offset of 16-byte chunk c of row r: the chunk index is XORed
@@ -344,13 +360,27 @@ struct KeysOnM {
       }
     }
   }
-  __device__ __forceinline__ void cap(float softcap, const float* mult, int lane) {
+  __device__ __forceinline__ void cap(float c, float inv, const float* mult, int lane) {
     const float2 f = *reinterpret_cast<const float2*>(mult + 2 * (lane & 3));
+    float most = 0.f;
 #pragma unroll
     for (int kg = 0; kg < KS / 16; ++kg)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s[kg][e] = capped(s[kg][e] * (e & 1 ? f.y : f.x), softcap * kLog2e);
+      for (int e = 0; e < 4; ++e) {
+        s[kg][e] *= e & 1 ? f.y : f.x;
+        most = fmaxf(most, fabsf(s[kg][e]));
+      }
+    if (__all_sync(~0u, most * inv < kCapNear)) {
+#pragma unroll
+      for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kg][e] = capped_near(s[kg][e], inv);
+    } else {
+#pragma unroll
+      for (int kg = 0; kg < KS / 16; ++kg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[kg][e] = capped(s[kg][e], c, inv);
+    }
   }
   template <bool LISTED>
   __device__ __forceinline__ void mask(const Sight<LISTED>& v, int lane) {
@@ -550,15 +580,33 @@ struct RowsOnM {
       for (int e = 0; e < 2; ++e) f.f[mt][e] = mult[mt * 16 + (lane >> 2) + 8 * e];
     return f;
   }
-  __device__ __forceinline__ void cap(float softcap, const float* mult, int lane) {
+  __device__ __forceinline__ void cap(float c, float inv, const float* mult, int lane) {
     const Factors f = factors(mult, lane);
+    float most = 0.f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < KS / 8; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s[mt][i][e] = capped(s[mt][i][e] * f.f[mt][e >> 1], softcap * kLog2e);
+        for (int e = 0; e < 4; ++e) {
+          s[mt][i][e] *= f.f[mt][e >> 1];
+          most = fmaxf(most, fabsf(s[mt][i][e]));
+        }
+    if (__all_sync(~0u, most * inv < kCapNear)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < KS / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][i][e] = capped_near(s[mt][i][e], inv);
+    } else {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < KS / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][i][e] = capped(s[mt][i][e], c, inv);
+    }
   }
   template <bool LISTED>
   __device__ __forceinline__ void mask(const Sight<LISTED>& v, int lane) {
@@ -712,7 +760,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_warp[W], s_pieces[W][4], s_lasts[C::kTeams][W];
   __shared__ int s_base, s_req, s_seg;
-  // log2 score per product (with a cap: its argument), and ones for capped scores
+  // log2 score per product, and ones for capped scores
   __shared__ __align__(8) float s_mults[C::kTeams][C::kRows], s_one[C::kRows];
   __shared__ int s_ends[C::kTeams][C::kRows];  // first key past a row's sight
   __shared__ float2 s_mls[C::kTeams][W][C::kRows];
@@ -810,7 +858,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   }
   // every CTA is running: the join may take the room of those that finish first
   pdl_launch_dependents();
-  const bool use_cap = a.softcap > 0.f;
+  const bool use_cap = a.cap_inv > 0.f;
 
   // units of setup that count in this call's segments
   const int setup = split && q == 0 ? kSetup : 0;
@@ -1032,7 +1080,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             if (QP * TT == C::kRows * LQ || r < C::kRows) {
               if (part == 0) {
                 // a masked score (-inf) times the factor must stay one: at least FLT_MIN
-                s_mult[r] = use_cap ? fabsf(mult) / a.softcap : fmaxf(fabsf(mult) * kLog2e, FLT_MIN);
+                s_mult[r] = fmaxf(fabsf(mult) * kLog2e, FLT_MIN);
                 s_one[r] = 1.f;  // every team's the same
                 s_end[r] = end0 + (row0 + r) / a.group;
               }
@@ -1140,7 +1188,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
             whole = ok && key0 + KS <= end0 &&
                     (a.window == 0 || key0 >= end0 + n_tok - 1 - a.window);
           }
-          if (use_cap) tile.cap(a.softcap, s_mult, lane);
+          if (use_cap) tile.cap(a.cap_log2, a.cap_inv, s_mult, lane);
           if (!whole) tile.mask(Sight<listed>{tab, s_end, tile0, key0, a.window}, lane);
 
           cp_async_wait_group<NS - 1>();

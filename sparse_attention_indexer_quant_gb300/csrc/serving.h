@@ -90,7 +90,8 @@ struct AttnArgs {
   unsigned long long* counter;  // generation-tagged count of claimed segments
   unsigned long long gen;       // this call's generation
   float scale;
-  float softcap;
+  float cap_log2;  // the cap in log2 units, and its reciprocal (0: no cap)
+  float cap_inv;
   int32_t window;
   int32_t topk;
   int32_t B;        // requests

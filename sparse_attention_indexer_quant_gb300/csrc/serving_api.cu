@@ -2,6 +2,7 @@
 // workspace layout and dispatch.  Nothing here allocates device memory or
 // synchronises.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -474,7 +475,11 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   a.part_ml = w.ml;
   a.part_o = w.o;
   a.scale = scale;
-  a.softcap = softcap;
+  if (softcap > 0.f) {
+    const double cap = (double)softcap * 1.4426950408889634;
+    a.cap_log2 = cap < FLT_MAX ? (float)cap : FLT_MAX;
+    a.cap_inv = (float)fmin(1.0 / cap, FLT_MAX);
+  }
   // a window no context can pass is none
   a.window = window >= max_blocks * kv->page_size ? 0 : window;
   a.topk = topk_idx ? topk : 0;
