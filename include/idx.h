@@ -548,7 +548,8 @@ IDX_API idx_status idx_qk_norm_rope_insert(
  * Scores, softmax statistics and sums are fp32 (a cap of any size adds at most
  * 2^-20 of the capped score); the weights enter the second
  * product as two 16-bit terms (over an fp16 or E4M3 cache weights below 2^-32 of
- * a row's highest count as zero; an infinite value in sight gives NaN).  Results do not depend on the order in which
+ * a row's highest count as zero; an infinite value in a row's sight gives NaN, one
+ * out of it does not reach the row).  Results do not depend on the order in which
  * blocks run.  Over-long contexts (clamped), negative ones (0) and page ids
  * outside the cache (their tokens are not seen) are counted in
  * errors->bad_inputs.

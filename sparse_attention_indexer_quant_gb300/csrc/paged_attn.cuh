@@ -284,6 +284,53 @@ struct Sight {
   }
 };
 
+// Whether one of a word's packed values is infinite or NaN (E4M3: NaN).
+template <int CT>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  if (CT == IDX_E4M3)  // a byte of all ones but the sign: the byte sum carries into its sign place
+    return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+  constexpr uint32_t e = CT == IDX_BF16 ? 0x7F80u : 0x7C00u, low = e & (0u - e);
+  return ((((w & (e | e << 16)) >> 1) + ((low | low << 16) >> 1)) & 0x40004000u) != 0;
+}
+
+// Keys that some of an item's rows see and others do not: a weight of zero times an
+// infinite or NaN value would be NaN, so a tile's such values become zeros, and
+// marks[row][dimension] says which sums of the rows that see them are to be NaN.
+// The keys are [lo0, lo1), past the later tokens' windows, and [hi0, hi1), the later
+// tokens' own: fewer than n_tok each, looked through 16 bytes a lane.  Costs 1 - 6 %
+// with several new tokens (128 contexts of 100 - 1000 keys, 3 tokens 58.3 -> 59.5 us,
+// 64 of 1000 - 8000, 4 tokens, E4M3 111.6 -> 113.7); with the NaN set in the sums
+// themselves, the tile's keys taken one by one, 60.9 and 119.2; rows done again
+// after a sum that is not finite 68.9 and 125.7 (the registers that must then outlive
+// the stream).
+template <int D, int CT, int ROWS>
+__device__ __forceinline__ void keep_apart(uint8_t* vt, const Sight<false>& v, int lo0, int lo1, int hi0,
+                                           int hi1, uint32_t (*marks)[D / 32], int* marked, int lane) {
+  constexpr int ROWB = D * (CT == IDX_E4M3 ? 1 : 2), CH = ROWB / 16;
+  const int lows = max(0, lo1 - lo0), n = lows + max(0, hi1 - hi0);
+  auto row_of = [&](int i) -> int { return (i < lows ? lo0 + i : hi0 + i - lows) - v.key0; };
+  bool bad = false;
+#pragma unroll 1
+  for (int c = lane; c < n * CH; c += 32) {
+    const uint4 x = *reinterpret_cast<const uint4*>(vt + swz<ROWB>(row_of(c / CH), c % CH));
+    bad = bad || not_finite<CT>(x.x) || not_finite<CT>(x.y) || not_finite<CT>(x.z) || not_finite<CT>(x.w);
+  }
+  if (!__any_sync(~0u, bad)) return;
+#pragma unroll 1
+  for (int i = lane; i < n * D; i += 32) {
+    const int kk = row_of(i / D), d = i % D, at = d * (CT == IDX_E4M3 ? 1 : 2);
+    uint8_t* p = vt + swz<ROWB>(kk, at >> 4) + (at & 15);
+    const uint32_t x = CT == IDX_E4M3 ? *p : *reinterpret_cast<uint16_t*>(p);
+    if (!not_finite<CT>(x)) continue;
+    if (CT == IDX_E4M3) *p = 0; else *reinterpret_cast<uint16_t*>(p) = 0;
+    *marked = 1;
+#pragma unroll 1
+    for (int r = 0; r < ROWS; ++r)
+      if (v.in(kk, r)) atomicOr(&marks[r][d / 32], 1u << (d % 32));
+  }
+  __syncwarp();
+}
+
 // Two weights of one row pair or key pair, as the fp16/bf16 term and the rest.
 template <bool MB>
 __device__ __forceinline__ void two_terms(float p0, float p1, uint32_t* hi, uint32_t* lo) {
@@ -760,6 +807,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_warp[W], s_pieces[W][4], s_lasts[C::kTeams][W];
   __shared__ int s_base, s_req, s_seg;
+  __shared__ uint32_t s_marks[listed ? 1 : C::kRows][D / 32];  // see keep_apart
+  __shared__ int s_marked;
   // log2 score per product, and ones for capped scores
   __shared__ __align__(8) float s_mults[C::kTeams][C::kRows], s_one[C::kRows];
   __shared__ int s_ends[C::kTeams][C::kRows];  // first key past a row's sight
@@ -859,6 +908,11 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   // every CTA is running: the join may take the room of those that finish first
   pdl_launch_dependents();
   const bool use_cap = a.cap_inv > 0.f;
+  auto clear_marks = [&]() {
+    for (int i = tid; i < C::kRows * (D / 32); i += TT) s_marks[0][i] = 0;
+    if (tid == 0) s_marked = 0;
+  };
+  if (!listed && a.next_n > 1) clear_marks();
 
   // units of setup that count in this call's segments
   const int setup = split && q == 0 ? kSetup : 0;
@@ -1189,10 +1243,17 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
                     (a.window == 0 || key0 >= end0 + n_tok - 1 - a.window);
           }
           if (use_cap) tile.cap(a.cap_log2, a.cap_inv, s_mult, lane);
-          if (!whole) tile.mask(Sight<listed>{tab, s_end, tile0, key0, a.window}, lane);
+          const Sight<listed> sight{tab, s_end, tile0, key0, a.window};
+          if (!whole) tile.mask(sight, lane);
 
           cp_async_wait_group<NS - 1>();
           __syncwarp();
+          if constexpr (!listed) {
+            if (!whole && n_tok > 1)
+              keep_apart<D, CT, C::kRows>(ring + get * C::kHalf, sight, max(lo_all, key0),
+                                          a.window > 0 ? min(end0 + min(n_tok - 1 - a.window, 0), key0 + KS) : 0,
+                                          max(end0, key0), min(sp.len, key0 + KS), s_marks, &s_marked, lane);
+          }
           tile.values(ring_u + get * C::kHalf, tile.factors(use_cap ? s_one : s_mult, lane), lane);
           __syncwarp();
           get = get + 1 == NS ? 0 : get + 1;
@@ -1217,6 +1278,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       if (split && ta == 0 && tid == TT - 1)
         a.desc[req * HR + hr] =
             make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(item_end - 1) - seg + 1);
+      const bool marked = !listed && n_tok > 1 && s_marked != 0;
       constexpr int QPR = D / 4;  // float4 quads per row
       for (int i = tid; i < rows * QPR; i += TT) {
         const int r = i / QPR, d = (i % QPR) * 4;
@@ -1236,6 +1298,14 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           acc.y += x.y * f;
           acc.z += x.z * f;
           acc.w += x.w * f;
+        }
+        if (marked) {
+          const uint32_t bits = s_marks[0][r * (D / 32) + d / 32] >> (d % 32);
+          const float nan = __int_as_float(0x7FFFFFFF);
+          if (bits & 1) acc.x = nan;
+          if (bits & 2) acc.y = nan;
+          if (bits & 4) acc.z = nan;
+          if (bits & 8) acc.w = nan;
         }
         if (complete) {
           const int rr = row0 + r;
@@ -1259,6 +1329,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
         }
       }
       sync();  // the rings, the table and the query rows are refilled next
+      if (marked) clear_marks();  // the next marks come after the table's barrier
 
       req = req_next;
     }
