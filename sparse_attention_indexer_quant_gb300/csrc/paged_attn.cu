@@ -31,7 +31,8 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, JoinRow w, int d, c
   const int tok = a.topk_idx ? w.req : w.req * a.next_n + w.rr / a.group;
   const int64_t orow = (int64_t)tok * a.Hq + w.h * a.group + w.rr % a.group;
   float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-  if (a.kv.dtype == IDX_E4M3 && a.kv.v_scale) inv *= __ldg(a.kv.v_scale + w.h);
+  // an empty row stays zero whatever the scale
+  if (a.kv.dtype == IDX_E4M3 && a.kv.v_scale && lsum != 0.f) inv *= __ldg(a.kv.v_scale + w.h);
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + orow * a.kv.head_dim + d);
 #pragma unroll
   for (int i = 0; i < N; i += 2)

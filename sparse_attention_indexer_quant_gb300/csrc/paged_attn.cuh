@@ -1311,7 +1311,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
           const int rr = row0 + r;
           const int64_t orow = (int64_t)(tok0 + rr / a.group) * a.Hq + h * a.group + rr % a.group;
           float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-          if (F8 && a.kv.v_scale) inv *= __ldg(a.kv.v_scale + h);
+          // an empty row stays zero whatever the scale
+          if (F8 && a.kv.v_scale && lsum != 0.f) inv *= __ldg(a.kv.v_scale + h);
           uint2 w;
           if (MB || (F8 && a.q_bf16)) {
             w.x = pack2<true>(acc.x * inv, acc.y * inv);
