@@ -476,8 +476,8 @@ IDX_API idx_status idx_plan_step(const int32_t* cached_lens, const int32_t* new_
  *   rot_dim    even, 2..256 (IDX_ROPE_NTK: 4..256); 0 <= pos0,
  *              pos0 + num_pos <= 2^31.
  * Angles are formed in 64-bit fixed point: beside the frequencies' own fp64
- * rounding they are off by at most 2^-31 of a turn at any position; values are then within
- * 2 * 2^-24 * mscale.
+ * rounding they are off by at most 2^-32 of a turn at any position.  Entries are
+ * then within 1.5 * 2^-24 where mscale is 1, else within 3.5 * 2^-24 * |mscale|.
  * ------------------------------------------------------------------------ */
 typedef enum {
   IDX_ROPE_NONE = 0,

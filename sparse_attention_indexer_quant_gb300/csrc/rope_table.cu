@@ -4,13 +4,14 @@
 // p * (w_i / 2 pi) mod 1, and with the frequency as a 64-bit fraction the
 // product and the reduction are one integer addition per row that wraps: no
 // fp64 arithmetic (which this chip runs at a small fraction of its fp32 rate)
-// and no loss at far positions.  The fraction's top 32 bits are split into a
-// quarter turn q and a remainder u in [-1, 1] eighths of a turn, whose sine and
-// cosine are polynomials in u^2: Chebyshev interpolation of sin(pi u / 4) / u
-// and cos(pi u / 4) over u^2 in [0, 1], degrees 3 and 4, off by 2.4e-9 and
-// 5e-11 before fp32 rounding (together under 1.5 * 2^-24).  With sincospif in
-// their place the kernel was bound by its instructions: 35 us for 262144 x 64
-// pairs (134 MB) against 22.8 us now.
+// and no loss at far positions.  The fraction is split into a quarter turn q and
+// 32 bits of remainder u in [-1, 1] eighths of a turn, whose sine and cosine are
+// polynomials in u^2: Chebyshev interpolation of sin(pi u / 4) / u and
+// cos(pi u / 4) over u^2 in [0, 1], degrees 3 and 4, off by 2.4e-9 and 5e-11
+// before fp32 rounding.  With u's rounding to fp32 and their own they are off by
+// at most 1.35 * 2^-24 (every fp32 u tried); the factor mscale adds its rounding
+// and the product's, 2^-24 each.  With sincospif in their place the kernel was
+// bound by its instructions: 35 us for 262144 x 64 pairs (134 MB) against 20.5 us now.
 //
 // Bound by its stores (8 bytes per pair): a thread owns four columns, walks
 // down the rows by adding its frequencies times the row step, and stores
@@ -24,12 +25,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ void cos_sin_turn(unsigned turn, float* c, float* s) {
-  const unsigned q = (turn + (1u << 29)) >> 30;               // nearest quarter, mod 4
-  const float u = (float)(int)(turn - (q << 30)) * 0x1p-29f;  // [-1, 1] eighths
+__device__ __forceinline__ void cos_sin_turn(unsigned long long phase, float* c, float* s) {
+  const unsigned turn = (unsigned)(phase >> 32);
+  const unsigned q = (turn + (1u << 29)) >> 30;  // nearest quarter, mod 4
+  // 32 bits of the rest: [-1, 1] eighths of a turn
+  const float u = (float)(int)__funnelshift_l((unsigned)phase, turn - (q << 30), 2) * 0x1p-31f;
   const float z = u * u;
-  const float sx = u * fmaf(fmaf(fmaf(-3.595429072400257e-05f, z, 0.002490006801490165f), z,
-                                 -0.08074543470810033f), z, 0.7853981609766182f);
+  // the sine's first term on its own, so that its sum is rounded once
+  const float sx = fmaf(u, 0.7853981609766182f,
+                        u * z * fmaf(fmaf(-3.595429072400257e-05f, z, 0.002490006801490165f), z,
+                                     -0.08074543470810033f));
   const float cx = fmaf(fmaf(fmaf(fmaf(3.5297971415016813e-06f, z, -0.00032593858595389604f), z,
                                   0.01585432522845092f), z, -0.3084251351582918f), z, 1.f);
   const float a = (q & 1) ? sx : cx, b = (q & 1) ? cx : sx;
@@ -59,7 +64,7 @@ __global__ void __launch_bounds__(kThreads) rope_table_kernel(const __grid_const
     float c[4], s[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      cos_sin_turn((unsigned)(turn[i] >> 32), &c[i], &s[i]);
+      cos_sin_turn(turn[i], &c[i], &s[i]);
       c[i] *= a.mscale;
       s[i] *= a.mscale;
       turn[i] += step[i];
