@@ -456,13 +456,24 @@ StepPlan = collections.namedtuple(
     "StepPlan", "context_lens query_start slot_mapping positions token_seq pool_head")
 
 
+class _NoServing:
+    """In the place of the compiled part where it is missing or does not load: the
+    other entries, which need ctypes alone, work; every serving call fails."""
+
+    def __init__(self, why: Exception):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise RuntimeError(
+            f"{name}: the serving binding is missing or does not load: build it first "
+            "(python -c 'import __graft_entry__ as g; g.build()')") from self._why
+
+
 def _load_serving():
     try:
         from . import _serving
     except ImportError as e:
-        raise RuntimeError(
-            "the serving binding is missing or does not load: build it first "
-            "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        return _NoServing(e)
     _serving.set_errors(IdxError, torch.OutOfMemoryError)
     return _serving
 

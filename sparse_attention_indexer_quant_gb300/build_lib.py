@@ -69,38 +69,45 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    def run(cmd, what):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    srcs = _sources()
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        ext = ex.submit(compile_serving, nvcc)
+        objs = list(ex.map(compile_one, srcs))
+    # libidx.so first: it does not depend on PyTorch, whatever becomes of the other
+    tmp = LIB + f".tmp{os.getpid()}"
+    _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], "link")
+    os.replace(tmp, LIB)
+    link_serving(*ext.result())
+    return LIB
 
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def compile_serving(nvcc):
+    """The binding's object file, and the folder of the PyTorch it was compiled against."""
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
-    ext_obj = os.path.join(BUILD, "serving_py.o")
-    ext_cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-               f"-I{INCLUDE}", f"-isystem{torch_dir}/include",
-               f"-isystem{torch_dir}/include/torch/csrc/api/include",
-               f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda_include}",
-               "-c", EXT_SOURCE, "-o", ext_obj]
-    srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        ext = ex.submit(run, ext_cmd, f"g++ on {EXT_SOURCE}")
-        objs = list(ex.map(compile_one, srcs))
-        ext.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+    obj = os.path.join(BUILD, "serving_py.o")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f"-I{INCLUDE}", f"-isystem{torch_dir}/include",
+          f"-isystem{torch_dir}/include/torch/csrc/api/include",
+          f"-isystem{sysconfig.get_paths()['include']}", f"-isystem{cuda_include}",
+          "-c", EXT_SOURCE, "-o", obj], f"g++ on {EXT_SOURCE}")
+    return obj, torch_dir
+
+
+def link_serving(obj, torch_dir):
     tmp = EXT + f".tmp{os.getpid()}"
-    run(["g++", "-shared", "-o", tmp, ext_obj, f"-L{HERE}", "-l:libidx.so", f"-L{torch_dir}/lib",
-         "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
-         "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_dir}/lib"], "link of the serving binding")
+    _run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libidx.so", f"-L{torch_dir}/lib",
+          "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
+          "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{torch_dir}/lib"], "link of the serving binding")
     os.replace(tmp, EXT)
-    return LIB
 
 
 if __name__ == "__main__":
