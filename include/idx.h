@@ -558,6 +558,22 @@ IDX_API idx_status idx_qk_norm_rope_insert(
 IDX_API size_t idx_paged_attention_workspace_bytes(int32_t B, int32_t next_n, int32_t Hq, int32_t Hkv,
                                            int32_t head_dim);
 
+/* How a call of these sizes shares its work out on a device of `sms` SMs (host
+ * only; topk = 0: whole contexts).  An item is a kv head of a request (with a
+ * selection, of a query row) with up to `rows` of its query rows. */
+typedef struct {
+  int32_t split;     /* 1: items cut along their keys over all CTAs and joined */
+  int32_t warps;     /* warps that share an item */
+  int32_t rows;      /* query rows of an item */
+  int32_t row_tiles; /* items a kv head's query rows make */
+  int32_t unit;      /* keys by which a split item is cut */
+  int32_t places;    /* items (split: CTAs) that run at once */
+} idx_attention_form;
+IDX_API idx_status idx_paged_attention_form(int32_t B, int32_t next_n, int32_t Hq, int32_t Hkv,
+                               int32_t head_dim, int32_t cache_dtype, int32_t page_size,
+                               int32_t max_blocks, int32_t topk, int32_t window, int32_t sms,
+                               idx_attention_form* form);
+
 IDX_API idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                int32_t dtype, int32_t B, int32_t next_n, int32_t Hq,
                                const idx_kv_cache* kv, const int32_t* block_table,

@@ -65,6 +65,7 @@ SIGNATURES = {
                                                _I64, _I32, _I32, _P, _P, _F32, _P, _P, _P, _I64,
                                                _I32, _I32, _P, _P, _P, _P, _P]),
     "idx_paged_attention_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32]),
+    "idx_paged_attention_form": (ctypes.c_int, [_I32] * 11 + [_P]),
     "idx_paged_attention": (ctypes.c_int, [_P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _I32,
                                            _P, _P, _I32, _F32, _F32, _I32, _P, _P, _P, _SZ, _P,
                                            _P]),
@@ -554,6 +555,28 @@ def qk_norm_rope_insert(q, k, v, q_weight, k_weight, eps: float, positions, cos,
 def paged_attention_workspace_bytes(B: int, next_n: int, Hq: int, Hkv: int,
                                     head_dim: int) -> int:
     return int(lib.idx_paged_attention_workspace_bytes(B, next_n, Hq, Hkv, head_dim))
+
+
+AttentionForm = collections.namedtuple("AttentionForm", "split warps rows row_tiles unit places")
+
+
+def paged_attention_form(B: int, next_n: int, Hq: int, Hkv: int, head_dim: int,
+                         cache_dtype=torch.bfloat16, page_size: int = PAGE_SIZE, max_blocks: int = 1,
+                         topk: int = 0, window: int = 0, sms: int | None = None) -> AttentionForm:
+    """How paged_attention shares out a call of these sizes on a device of `sms` SMs
+    (None: the current device): items cut along their keys over all CTAs and joined
+    (split), or whole by teams of `warps` warps; items' query rows, items a kv head's
+    rows make, keys by which a split item is cut, and items or CTAs that run at once."""
+    if sms is None:
+        sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    kinds = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+    if cache_dtype not in kinds:
+        raise TypeError("cache_dtype must be bfloat16, float16 or float8_e4m3fn")
+    form = (ctypes.c_int32 * 6)()
+    _check("idx_paged_attention_form",
+           lib.idx_paged_attention_form(B, next_n, Hq, Hkv, head_dim, kinds[cache_dtype], page_size,
+                                        max_blocks, topk, window, sms, form))
+    return AttentionForm(bool(form[0]), *form[1:])
 
 
 def paged_attention(q, k_cache, v_cache, block_table, context_lens, next_n: int = 1,

@@ -172,6 +172,40 @@ int attn_warps(int64_t items, double bytes, bool listed, int ctas, int occ, int 
   return warps;
 }
 
+// How a call shares its items out.
+struct AttnForm {
+  int rows, nt, part_rows, row_tiles;  // query rows of a kv head, in tiles of eight, an item's, items a head
+  int window;                          // 0 where no context can pass it
+  int unit, ctas;                      // keys of a CTA's unit, CTAs the device holds at once
+  int64_t keys, items, units, grid;    // keys an item can have at most
+  int warps;                           // that share an item
+  bool split;
+};
+AttnForm attn_form(int64_t B, int next_n, int group, int heads, int D, int dtype, int page_size,
+                   int max_blocks, int topk, int window, int sms) {
+  AttnForm f;
+  const int elt = dtype == IDX_E4M3 ? 1 : 2;
+  f.rows = topk > 0 ? group : group * next_n;
+  f.nt = idx::attn_row_tiles(D, f.rows);
+  f.part_rows = (int)part_rows_of(D, f.rows);
+  f.row_tiles = (f.rows + 8 * f.nt - 1) / (8 * f.nt);
+  f.window = window >= max_blocks * page_size ? 0 : window;
+  f.unit = idx::attn_unit_keys(D, dtype, f.nt);
+  f.keys = topk > 0 ? topk : (int64_t)max_blocks * page_size;
+  if (topk == 0 && f.window > 0 && f.keys > (int64_t)f.window + next_n + f.unit)
+    f.keys = (int64_t)f.window + next_n + f.unit;  // sight of all rows, first unit cut
+  f.units = (f.keys + f.unit - 1) / f.unit;
+  f.items = (topk > 0 ? B * next_n : B) * heads * f.row_tiles;
+  const int occ = idx::attn_occupancy(D, dtype, f.nt);
+  f.ctas = sms * occ < idx::kAttnMaxCtas ? sms * occ : idx::kAttnMaxCtas;
+  const int warps = attn_warps(f.items, (double)f.keys * D * 2 * elt, topk > 0, f.ctas, occ, f.nt,
+                               dtype == IDX_E4M3);
+  f.split = f.units > 2 && warps == 0;
+  f.warps = warps == 0 ? 8 : warps;
+  f.grid = f.split ? (f.units * f.items < f.ctas ? f.units * f.items : f.ctas) : f.items;
+  return f;
+}
+
 bool attn_shape_ok(int64_t B, int64_t next_n, int64_t Hq, int64_t Hkv, int D) {
   return B >= 0 && B <= 65535 && next_n >= 1 && next_n <= 16 && Hkv >= 1 && Hkv <= 1024 &&
          Hq >= Hkv && Hq <= 4096 && Hq % Hkv == 0 && (D == 64 || D == 128 || D == 256) &&
@@ -394,6 +428,29 @@ size_t idx_paged_attention_workspace_bytes(int32_t B, int32_t next_n, int32_t Hq
   return attn_ws(nullptr, B, next_n, Hq, Hkv, head_dim, nullptr);
 }
 
+idx_status idx_paged_attention_form(int32_t B, int32_t next_n, int32_t Hq, int32_t Hkv,
+                                    int32_t head_dim, int32_t cache_dtype, int32_t page_size,
+                                    int32_t max_blocks, int32_t topk, int32_t window, int32_t sms,
+                                    idx_attention_form* form) {
+  if (!form) return fail(IDX_ERR_INVALID_ARG, "null form");
+  if (!attn_shape_ok(B, next_n, Hq, Hkv, head_dim))
+    return fail(IDX_ERR_INVALID_ARG, "B=%d, next_n=%d, Hq=%d, Hkv=%d, head_dim=%d", B, next_n, Hq, Hkv, head_dim);
+  if (cache_dtype < IDX_BF16 || cache_dtype > IDX_E4M3)
+    return fail(IDX_ERR_INVALID_ARG, "cache dtype=%d", cache_dtype);
+  if (page_shift_of(page_size) < 0)
+    return fail(IDX_ERR_INVALID_ARG, "page_size=%d (16, 32, 64 or 128)", page_size);
+  if (max_blocks <= 0 || max_blocks > (INT32_MAX - 4096) / page_size)
+    return fail(IDX_ERR_INVALID_ARG, "max_blocks=%d", max_blocks);
+  if (topk < 0 || topk > (1 << 20) || window < 0 || (topk > 0 && window > 0))
+    return fail(IDX_ERR_INVALID_ARG, "topk=%d, window=%d", topk, window);
+  if (sms < 1 || sms > 1024) return fail(IDX_ERR_INVALID_ARG, "sms=%d", sms);
+  const AttnForm f = attn_form(B, next_n, Hq / Hkv, Hkv, head_dim, cache_dtype, page_size, max_blocks,
+                               topk, window, sms);
+  *form = idx_attention_form{f.split, f.warps, f.part_rows, f.row_tiles, f.unit,
+                             f.split ? (int32_t)f.grid : f.ctas * 8 / f.warps};
+  return ok();
+}
+
 idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                                int32_t dtype, int32_t B, int32_t next_n, int32_t Hq,
                                const idx_kv_cache* kv, const int32_t* block_table,
@@ -480,17 +537,17 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
     a.cap_log2 = cap < FLT_MAX ? (float)cap : FLT_MAX;
     a.cap_inv = (float)fmin(1.0 / cap, FLT_MAX);
   }
-  // a window no context can pass is none
-  a.window = window >= max_blocks * kv->page_size ? 0 : window;
+  const AttnForm f = attn_form(B, next_n, Hq / kv->heads, kv->heads, D, kv->dtype, kv->page_size,
+                               max_blocks, topk_idx ? topk : 0, window, sms);
+  a.window = f.window;
   a.topk = topk_idx ? topk : 0;
   a.B = B;
   a.next_n = next_n;
   a.Hq = Hq;
   a.group = Hq / kv->heads;
-  a.rows = topk_idx ? a.group : a.group * next_n;
-  const int nt = idx::attn_row_tiles(D, a.rows);
-  a.part_rows = (int32_t)part_rows_of(D, a.rows);
-  a.row_tiles = (a.rows + 8 * nt - 1) / (8 * nt);
+  a.rows = f.rows;
+  a.part_rows = f.part_rows;
+  a.row_tiles = f.row_tiles;
   a.max_blocks = max_blocks;
   a.page_shift = page_shift_of(kv->page_size);
   a.off_shift = off_shift;
@@ -499,26 +556,12 @@ idx_status idx_paged_attention(const void* q, int64_t q_token_stride, int64_t q_
   a.q_bf16 = dtype == IDX_BF16;
   a.errors = errors;
 
-  // Units an item can have at most, the CTAs the device holds at once, and how
-  // items are shared out.
-  const int unit = idx::attn_unit_keys(D, kv->dtype, nt);
-  int64_t keys = topk_idx ? topk : (int64_t)max_blocks * kv->page_size;
-  if (!topk_idx && a.window > 0 && keys > (int64_t)a.window + next_n + unit)
-    keys = (int64_t)a.window + next_n + unit;  // sight of all rows, first unit cut
-  const int64_t units = (keys + unit - 1) / unit;
-  const int64_t items = (int64_t)(topk_idx ? B * next_n : B) * kv->heads * a.row_tiles;
-  const int occ = idx::attn_occupancy(D, kv->dtype, nt);
-  int64_t ctas = (int64_t)sms * occ;
-  if (ctas > idx::kAttnMaxCtas) ctas = idx::kAttnMaxCtas;
-  const int warps = attn_warps(items, (double)keys * D * 2 * elt, topk_idx != nullptr, (int)ctas, occ, nt,
-                               kv->dtype == IDX_E4M3);
-  a.split = units > 2 && warps == 0;
-  a.warps = warps == 0 ? 8 : warps;
-  const int64_t grid = a.split ? (units * items < ctas ? units * items : ctas) : items;
-  if ((units + 64) * items > INT32_MAX || items * a.part_rows > INT32_MAX)
+  if ((f.units + 64) * f.items > INT32_MAX || f.items * f.part_rows > INT32_MAX)
     return fail(IDX_ERR_INVALID_ARG, "%lld query row tiles of up to %lld keys: too much for one call",
-                (long long)items, (long long)keys);
-  a.grid = (int32_t)grid;
+                (long long)f.items, (long long)f.keys);
+  a.split = f.split;
+  a.warps = f.warps;
+  a.grid = (int32_t)f.grid;
   cudaError_t e = kv->dtype == IDX_BF16   ? idx::launch_attn_bf16(a, (cudaStream_t)stream)
                   : kv->dtype == IDX_FP16 ? idx::launch_attn_fp16(a, (cudaStream_t)stream)
                                           : idx::launch_attn_e4m3(a, (cudaStream_t)stream);
