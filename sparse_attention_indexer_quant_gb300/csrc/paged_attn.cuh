@@ -297,12 +297,12 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
 // infinite or NaN value would be NaN, so a tile's such values become zeros, and
 // marks[row][dimension] says which sums of the rows that see them are to be NaN.
 // The keys are [lo0, lo1), past the later tokens' windows, and [hi0, hi1), the later
-// tokens' own: fewer than n_tok each, looked through 16 bytes a lane.  Costs 1 - 6 %
-// with several new tokens (128 contexts of 100 - 1000 keys, 3 tokens 58.3 -> 59.5 us,
-// 64 of 1000 - 8000, 4 tokens, E4M3 111.6 -> 113.7); with the NaN set in the sums
-// themselves, the tile's keys taken one by one, 60.9 and 119.2; rows done again
-// after a sum that is not finite 68.9 and 125.7 (the registers that must then outlive
-// the stream).
+// tokens' own: fewer than n_tok each, looked through 16 bytes a lane.  Calls of several
+// tokens pay 0 - 6 % for it (64 contexts of 100 - 500 keys, 2 tokens 13.6 -> 14.2 us,
+// 64 of 1000 - 8000, 4 tokens, E4M3 111 -> 113); with the NaN set in the sums
+// themselves, the tile's keys taken one by one, 14.2 and 119; rows done again after a
+// sum that is not finite 14.4 and 126 (registers that must then outlive the stream).
+// In kernels of its own: as a branch of one kernel it cost calls of one token up to 6 %.
 template <int D, int CT, int ROWS>
 __device__ __forceinline__ void keep_apart(uint8_t* vt, const Sight<false>& v, int lo0, int lo1, int hi0,
                                            int hi1, uint32_t (*marks)[D / 32], int* marked, int lane) {
@@ -798,7 +798,8 @@ struct TileOf<D, CT, 1, KS> {
   using type = KeysOnM<D, CT, KS>;
 };
 
-template <int D, int CT, int NT, bool listed, int W>
+// several: more than one new token a request, whose sights differ (whole contexts)
+template <int D, int CT, int NT, bool listed, int W, bool several>
 __global__ void __launch_bounds__((Cfg<D, CT, NT, listed, W>::kThreads), (Cfg<D, CT, NT, listed, W>::kCtas))
 paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   using C = Cfg<D, CT, NT, listed, W>;
@@ -807,7 +808,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ int s_warp[W], s_pieces[W][4], s_lasts[C::kTeams][W];
   __shared__ int s_base, s_req, s_seg;
-  __shared__ uint32_t s_marks[listed ? 1 : C::kRows][D / 32];  // see keep_apart
+  __shared__ uint32_t s_marks[several ? C::kRows : 1][D / 32];  // see keep_apart
   __shared__ int s_marked;
   // log2 score per product, and ones for capped scores
   __shared__ __align__(8) float s_mults[C::kTeams][C::kRows], s_one[C::kRows];
@@ -912,7 +913,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
     for (int i = tid; i < C::kRows * (D / 32); i += TT) s_marks[0][i] = 0;
     if (tid == 0) s_marked = 0;
   };
-  if (!listed && a.next_n > 1) clear_marks();
+  if (several) clear_marks();
 
   // units of setup that count in this call's segments
   const int setup = split && q == 0 ? kSetup : 0;
@@ -1248,8 +1249,8 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
 
           cp_async_wait_group<NS - 1>();
           __syncwarp();
-          if constexpr (!listed) {
-            if (!whole && n_tok > 1)
+          if constexpr (several) {
+            if (!whole)
               keep_apart<D, CT, C::kRows>(ring + get * C::kHalf, sight, max(lo_all, key0),
                                           a.window > 0 ? min(end0 + min(n_tok - 1 - a.window, 0), key0 + KS) : 0,
                                           max(end0, key0), min(sp.len, key0 + KS), s_marks, &s_marked, lane);
@@ -1278,7 +1279,7 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
       if (split && ta == 0 && tid == TT - 1)
         a.desc[req * HR + hr] =
             make_int2(part, q > 0 ? (units + q - 1) / q : cut.owner(item_end - 1) - seg + 1);
-      const bool marked = !listed && n_tok > 1 && s_marked != 0;
+      const bool marked = several && s_marked != 0;
       constexpr int QPR = D / 4;  // float4 quads per row
       for (int i = tid; i < rows * QPR; i += TT) {
         const int r = i / QPR, d = (i % QPR) * 4;
@@ -1344,47 +1345,47 @@ paged_attn_kernel(const __grid_constant__ AttnArgs a) {
   }
 }
 
-template <int D, int CT, int NT, bool listed, int W>
+template <int D, int CT, int NT, bool listed, int W, bool several>
 cudaError_t launch_items(const AttnArgs& a, cudaStream_t stream) {
   using C = Cfg<D, CT, NT, listed, W>;
-  auto kern = paged_attn_kernel<D, CT, NT, listed, W>;
+  auto kern = paged_attn_kernel<D, CT, NT, listed, W, several>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3((a.grid + C::kTeams - 1) / C::kTeams), dim3(C::kThreads), C::kSmem,
                           stream, a);
 }
 
-template <int D, int CT, int NT, int W>
-cudaError_t launch_team(const AttnArgs& a, cudaStream_t stream) {
-  return a.topk_idx ? launch_items<D, CT, NT, true, W>(a, stream) : launch_items<D, CT, NT, false, W>(a, stream);
-}
+// A call's kernels by what its items see: one token's context each, several tokens'
+// contexts, a selection.
+enum Sights : int { kOneToken = 0, kSeveralTokens = 1, kSelection = 2 };
 
-template <int D, int CT, int NT>
+template <int D, int CT, int NT, int S>
 cudaError_t launch(const AttnArgs& a, cudaStream_t stream) {
+  constexpr bool listed = S == kSelection, several = S == kSeveralTokens;
   switch (a.warps) {
-    case 1: return launch_team<D, CT, NT, 1>(a, stream);
-    case 2: return launch_team<D, CT, NT, 2>(a, stream);
-    case 4: return launch_team<D, CT, NT, 4>(a, stream);
+    case 1: return launch_items<D, CT, NT, listed, 1, several>(a, stream);
+    case 2: return launch_items<D, CT, NT, listed, 2, several>(a, stream);
+    case 4: return launch_items<D, CT, NT, listed, 4, several>(a, stream);
   }
-  return launch_team<D, CT, NT, kWarps>(a, stream);
+  return launch_items<D, CT, NT, listed, kWarps, several>(a, stream);
 }
 
-template <int D, int CT>
+template <int D, int CT, int S>
 cudaError_t launch_rows(const AttnArgs& a, cudaStream_t stream) {
   switch (attn_row_tiles(D, a.rows)) {
-    case 1: return launch<D, CT, 1>(a, stream);
-    case 2: return launch<D, CT, 2>(a, stream);
+    case 1: return launch<D, CT, 1, S>(a, stream);
+    case 2: return launch<D, CT, 2, S>(a, stream);
   }
-  if constexpr (D <= 128) return launch<D, CT, 4>(a, stream);
+  if constexpr (D <= 128) return launch<D, CT, 4, S>(a, stream);
   return cudaErrorInvalidValue;
 }
 
-template <int CT>
+template <int CT, int S>
 cudaError_t launch_type(const AttnArgs& a, cudaStream_t stream) {
   switch (a.kv.head_dim) {
-    case 64: return launch_rows<64, CT>(a, stream);
-    case 128: return launch_rows<128, CT>(a, stream);
-    default: return launch_rows<256, CT>(a, stream);
+    case 64: return launch_rows<64, CT, S>(a, stream);
+    case 128: return launch_rows<128, CT, S>(a, stream);
+    default: return launch_rows<256, CT, S>(a, stream);
   }
 }
 

@@ -3,6 +3,8 @@
 
 namespace idx {
 cudaError_t launch_attn_fp16(const AttnArgs& a, cudaStream_t stream) {
-  return attn::launch_type<IDX_FP16>(a, stream);
+  if (a.topk_idx) return attn::launch_type<IDX_FP16, attn::kSelection>(a, stream);
+  return a.next_n > 1 ? launch_attn_fp16_several(a, stream)
+                      : attn::launch_type<IDX_FP16, attn::kOneToken>(a, stream);
 }
 }  // namespace idx

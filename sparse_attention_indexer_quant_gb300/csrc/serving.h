@@ -134,6 +134,10 @@ constexpr int attn_unit_keys(int head_dim, int cache_dtype, int nt) {
 cudaError_t launch_attn_bf16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_fp16(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_e4m3(const AttnArgs& a, cudaStream_t stream);
+// whole contexts, several new tokens a request (translation units of their own)
+cudaError_t launch_attn_bf16_several(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_fp16_several(const AttnArgs& a, cudaStream_t stream);
+cudaError_t launch_attn_e4m3_several(const AttnArgs& a, cudaStream_t stream);
 cudaError_t launch_attn_join(const AttnArgs& a, cudaStream_t stream);
 
 }  // namespace idx

@@ -175,16 +175,18 @@ def way_of(idx, problem, lens=None, sms=None):
 
 # Shapes of whole and split calls for every kernel: (requests, kv heads, keys) tried in
 # this order until one is shared out as asked for.
-GROUPS = {1: (3, 2), 2: (6, 2), 4: (10, 2)}           # row tiles: heads a kv head, tokens
-LISTED_GROUPS = {1: (5, 1), 2: (13, 1), 4: (24, 1)}
+GROUPS = {"several": {1: (3, 2), 2: (6, 2), 4: (10, 2)},  # row tiles: heads a kv head, tokens
+          "one": {1: (5, 1), 2: (13, 1), 4: (24, 1)}, "listed": {1: (5, 1), 2: (13, 1), 4: (24, 1)}}
 SHAPES = [(2, 1, 4000), (2, 1, 2000), (2, 2, 700), (3, 2, 300), (2, 1, 200), (20, 10, 300), (20, 16, 96),
           (5, 40, 300), (2, 160, 96), (40, 8, 300), (80, 8, 96), (80, 8, 48), (40, 20, 96), (160, 8, 96),
           (160, 8, 48), (160, 8, 16), (320, 8, 40), (320, 8, 16), (320, 10, 16)]
 
 
-def shape_for(idx, D, cache, tiles, listed, warps, sms=None):
-    """Problem's arguments of a call that is shared out by `warps` (0: split)."""
-    group, next_n = (LISTED_GROUPS if listed else GROUPS)[tiles]
+def shape_for(idx, D, cache, tiles, sights, warps, sms=None):
+    """Problem's arguments of a call that is shared out by `warps` (0: split); sights:
+    one new token a request, several, or selections."""
+    group, next_n = GROUPS[sights][tiles]
+    listed = sights == "listed"
     for B, heads, keys in SHAPES:
         if heads * group > 4096:
             continue
@@ -198,6 +200,6 @@ def shape_for(idx, D, cache, tiles, listed, warps, sms=None):
     return None
 
 
-FORMS = [(D, cache, tiles, listed, warps) for D in (64, 128, 256) for cache in TYPES
-         for tiles in ((1, 2, 4) if D < 256 else (1, 2)) for listed in (False, True)
+FORMS = [(D, cache, tiles, sights, warps) for D in (64, 128, 256) for cache in TYPES
+         for tiles in ((1, 2, 4) if D < 256 else (1, 2)) for sights in GROUPS
          for warps in (0, 8, 4, 2, 1)]

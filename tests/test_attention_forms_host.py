@@ -38,9 +38,9 @@ def test_form_refuses(idx, bad):
     assert idx.lib.idx_paged_attention_form(1, 1, 8, 8, 128, 0, 64, 4, 0, 0, SMS, None) == 1
 
 
-@pytest.mark.parametrize("D,cache,tiles,listed,warps", af.FORMS)
-def test_a_shape_reaches_every_kernel(idx, D, cache, tiles, listed, warps):
-    assert af.shape_for(idx, D, cache, tiles, listed, warps, SMS)
+@pytest.mark.parametrize("D,cache,tiles,sights,warps", af.FORMS)
+def test_a_shape_reaches_every_kernel(idx, D, cache, tiles, sights, warps):
+    assert af.shape_for(idx, D, cache, tiles, sights, warps, SMS)
 
 
 @pytest.mark.parametrize("name", list(af.WAYS))

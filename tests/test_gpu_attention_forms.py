@@ -34,15 +34,15 @@ def check(idx, p, softcap=0.0, window=0, ref=None, **more):
     return out, lse
 
 
-@pytest.mark.parametrize("D,cache,tiles,listed,warps", af.FORMS)
-def test_every_kernel(idx, D, cache, tiles, listed, warps):
-    args = af.shape_for(idx, D, cache, tiles, listed, warps)
+@pytest.mark.parametrize("D,cache,tiles,sights,warps", af.FORMS)
+def test_every_kernel(idx, D, cache, tiles, sights, warps):
+    args = af.shape_for(idx, D, cache, tiles, sights, warps)
     if args is None:
         pytest.skip("no shape for this number of SMs")
     p = af.Problem(**args)
     form = idx.paged_attention_form(*p.form_args)
     assert (0 if form.split else form.warps) == warps
-    assert form.rows * form.row_tiles >= p.q.shape[1] // p.heads * (1 if listed else p.next_n)
+    assert form.rows * form.row_tiles >= p.q.shape[1] // p.heads * p.next_n
     check(idx, p)
     check(idx, p, softcap=20.0)
 
