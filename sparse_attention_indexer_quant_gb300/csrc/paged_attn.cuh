@@ -178,8 +178,9 @@ __device__ __forceinline__ float ex2(float x) {
 // large the cap is (a cap past every score changes nothing); above, tanh(y) =
 // 1 - 2 / (1 + e^2y) with the exponential's and the reciprocal's 2^-22.  In all
 // at most 2^-20 of the score.  The second form alone is off by 2^-21 of the cap.
-// A tile whose scores are all below takes the first form alone (ragged capped case
-// 21.0 us, both forms and a choice for every score 22.8, the second alone 20.4).
+// A tile whose scores are all below takes the first form alone (37 ragged contexts,
+// fp16, 16 rows 21.0 us; both forms and a choice for every score 22.8, the second
+// form alone 20.4).
 constexpr float kCapNear = 0.5f;
 __device__ __forceinline__ float capped_near(float x, float inv) {
   const float y = x * inv, z = y * y;

@@ -13,8 +13,9 @@
 // of 256 tokens and of 256 pages: one launch, no communication between blocks.
 // A decode batch is one or two blocks and its time is launch plus four
 // dependent round trips (lengths, sums, page, store); the bytes of a step
-// (16 per token) never bound it.  A call takes 6.2 us for 256 decode requests
-// and 7.2 us for 129 requests with 64K new tokens, most of it on the host.
+// (16 per token) never bound it.  A call takes 6.6 us for 256 decode requests and
+// 7.4 us for 129 requests with 64K new tokens, most of it on the host (replayed in
+// a graph 3.9 and 4.7; 3.6 and 195 where the lengths advance in place).
 #include "common.cuh"
 #include "launch.h"
 #include "serving.h"

@@ -130,8 +130,9 @@ int common_shift(int64_t x, int64_t y) {
 // and a last wave of few items costs its whole time.  Contexts are taken to fill
 // half of their room on average, and the longest, which may come last, costs 0.4 of
 // its time.  Over 277 measured cases of types, head layouts and lengths this choice
-// takes 1.7 % more time than the best of the five on average (26 % at most) and
-// 13 % less than splitting always (14 % more at most).
+// takes 1.7 % more time than the best of the five on average (26 % at most, where
+// contexts fill little of their room) and 13 % less than splitting always (14 % more
+// at most).
 //   us (8 heads, 8 rows of 128, bf16)     split   8 warps   4     2     1
 //   64 x 2048 selected                      94      88      86   100   153
 //   80 x 2048 selected                     113     120     135   116   162
