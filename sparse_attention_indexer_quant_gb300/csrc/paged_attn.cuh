@@ -34,8 +34,8 @@
 // bf16 value within 2^-29 of the row's largest.  4-bit codes (E2M1, one power of two 2^e
 // per 32 dimensions) are exact in both types: keys in fp16, a block's part of a score
 // times its key's 2^e in fp32 after the products over the block; values in bf16, the
-// weights' terms times 2^e before the product (exact, bf16 having fp32's range; values up to
-// 2^54 leave room for the weights').
+// weights' terms times 2^e before the product (exact, bf16 having fp32's range; values from
+// scale byte 0 up to 2^54 leave room for the weights').
 //
 // Memory.  2 G flops per byte of cache (G query heads per kv head) is far
 // below the tensor pipes' ridge, so the kernel is built as a stream: each of
@@ -51,8 +51,8 @@
 // 94).  Rows gathered one by one take 0.92 of the copy rate at 256 bytes, 0.95 at
 // 512, 0.70 - 0.74 at 128.  The tensor pipe is 13 - 15 % busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
 // from 32 rows over an E4M3 cache on (0.53 of the copy rate).  Over 4-bit values the logic
-// pipe binds: 64 requests of 20480 keys 364 us, 0.58 of the copy rate, that pipe 61 % and the
-// issue slots 69 % busy (440 instructions for 16 keys of 128 dimensions, half of them to
+// pipe binds: 64 requests of 20480 keys 383 us, 0.55 of the copy rate, that pipe 59 % and the
+// issue slots 72 % busy (476 instructions for 16 keys of 128 dimensions, half of them to
 // turn codes into operands); selected positions by two places gathered a row, codes and scales.
 #pragma once
 
@@ -74,13 +74,12 @@ constexpr uint32_t kNone = 0xFFFFFFFFu;
 constexpr float kSlack = 8.f;  // log2 of how far a score may pass the highest at the last raise
 // log2 of the weight that a raise gives the highest score: with fp16 operands as
 // high as their range allows (2^15 after the slack), since what lies under 2^-25
-// is lost: 2^-32 of the highest weight and less
-// over 4-bit values, which enter the product as 2^-126 of themselves, 2^64 of bf16's range
-// (sums that leave are brought back by the rest, and so are the weights' sums).
+// is lost: 2^-32 of the highest weight and less.  Over 4-bit values 2^32, so that the second
+// term of a weight times a scale byte's 2^-127 is still a normal number, and 2^31 keys' weights of
+// up to 2^40 times values of 2^54 are finite (brought back when the sums leave).
 template <bool PB, bool F4 = false>
-constexpr float kLift = F4 ? 64.f : (PB ? 0.f : 7.f);
-constexpr float kCodeUp = 4.611686018427388e18f;        // 2^62
-constexpr float kLiftDown = 5.421010862427522e-20f;     // 2^-64
+constexpr float kLift = F4 ? 32.f : (PB ? 0.f : 7.f);
+constexpr float kLiftDown = 2.3283064365386963e-10f;  // 2^-32
 
 template <int D, int CT>
 constexpr int row_bytes() { return attn_row_bytes(D, CT); }  // of codes or values
@@ -335,7 +334,7 @@ template <int D>
 __device__ __forceinline__ uint32_t scale_word(uint32_t scales, int key, int w) {
   return D == 64 ? lds16(scales + key * 2) : lds32(scales + key * (D / 32) + 4 * w);
 }
-// 2^e of a word's byte b (of a byte of 0: zero, such a block holds zeros).
+// 2^e of a word's byte b (of a byte of 0: zero, such a block of a key counts as zeros).
 __device__ __forceinline__ float scale_of(uint32_t w, int b) {
   return __uint_as_float((b < 3 ? w << (23 - 8 * b) : w >> 1) & 0x7F800000u);
 }
@@ -352,17 +351,20 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 // Of a word with four codes of one key below four of another: the pairs of the same
-// place, in bf16, as 2^-126 of their values (the least of them a subnormal number, which the
-// tensor core takes as it is; the sums are brought back when they leave).  A code's three low
-// bits moved to a bf16's bits 6 - 8 are just that; its sign is six places further up, so one
+// place, in bf16.  A code's three low bits moved to a bf16's bits 6 - 8 are 2^-126 of its
+// value (the least of them a subnormal number); its sign is six places further up, so one
 // multiplication by 65 moves both (products run beside the logic operations, which bind).
+// A product with 2^126 gives the value itself: left to the sums, the factor would cost the small
+// values their bits there (64 contexts of 20480 keys 365 us, 383 with it: those of 2^-64 came short of
+// some, from 2^-87 on they were zero.  A power of two per block of dimensions that follows the
+// scale bytes as the reference follows the scores: 376, and small values beside large ones still lost).
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
-  constexpr uint32_t keep = 0x81C081C0u;
+  constexpr uint32_t keep = 0x81C081C0u, up = 0x7E807E80u;  // 2^126
   const uint32_t u = w >> 8;
-  v[0] = ((w & 0x000F000Fu) * (65u << 6)) & keep;
-  v[1] = ((w & 0x00F000F0u) * (65u << 2)) & keep;
-  v[2] = ((u & 0x000F000Fu) * (65u << 6)) & keep;
-  v[3] = ((u & 0x00F000F0u) * (65u << 2)) & keep;
+  v[0] = mul_bf16x2(((w & 0x000F000Fu) * (65u << 6)) & keep, up);
+  v[1] = mul_bf16x2(((w & 0x00F000F0u) * (65u << 2)) & keep, up);
+  v[2] = mul_bf16x2(((u & 0x000F000Fu) * (65u << 6)) & keep, up);
+  v[3] = mul_bf16x2(((u & 0x00F000F0u) * (65u << 2)) & keep, up);
 }
 // The scale words of N keys for two blocks' worth of code chunks (c2), loaded once for
 // every four blocks.
@@ -697,8 +699,8 @@ struct KeysOnM {
           if (F4) {
             if (i % 2 == 0)
               *reinterpret_cast<float4*>(buf + r * pitch + i * 16 + 4 * g) =
-                  make_float4(o[i][e] * kCodeUp, o[i][2 + e] * kCodeUp, o[(i + 1) % (D / 16)][e] * kCodeUp,
-                              o[(i + 1) % (D / 16)][2 + e] * kCodeUp);
+                  make_float4(o[i][e] * kLiftDown, o[i][2 + e] * kLiftDown, o[(i + 1) % (D / 16)][e] * kLiftDown,
+                              o[(i + 1) % (D / 16)][2 + e] * kLiftDown);
           } else if (F8) {
             *reinterpret_cast<float2*>(buf + r * pitch + i * 16 + 2 * g) = make_float2(o[i][e], o[i][2 + e]);
           } else {
@@ -1013,8 +1015,8 @@ struct RowsOnM {
               // columns 2 c4, 2 c4 + 1 of four products: eight dimensions in turn
               const int f = i & ~3, k = (i & 2) / 2;
               *reinterpret_cast<float4*>(row + f * 8 + 8 * c4 + 4 * k) =
-                  make_float4(o[mt][f][2 * e + k] * kCodeUp, o[mt][f + 1][2 * e + k] * kCodeUp,
-                              o[mt][f + 2][2 * e + k] * kCodeUp, o[mt][f + 3][2 * e + k] * kCodeUp);
+                  make_float4(o[mt][f][2 * e + k] * kLiftDown, o[mt][f + 1][2 * e + k] * kLiftDown,
+                              o[mt][f + 2][2 * e + k] * kLiftDown, o[mt][f + 3][2 * e + k] * kLiftDown);
             } else if (F8) {
               *reinterpret_cast<float4*>(row + i * 8 + 4 * c4) =
                   make_float4(o[mt][i][2 * e], o[mt][i + 1][2 * e], o[mt][i][2 * e + 1],
