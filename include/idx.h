@@ -635,12 +635,15 @@ IDX_API idx_status idx_gather_kv(const idx_kv_cache* kv, const int32_t* block_ta
  *              -inf.  Rows outside all sequences are left as they were.  out may not
  *              overlap k, v or (but for q itself, where q is contiguous) q.
  * Scores, softmax statistics and sums are fp32 (scores must stay below 2^24, where an
- * fp32 rounding is a factor in the weight; a cap adds at most 2^-20 of the capped score); each weight is rounded to q's type before it meets its value (by up to 2^-8 of
- * itself in bf16, 2^-11 in fp16, small ones there by 2^-28 of the row's highest).  An infinite or NaN value in a row's sight makes that output
- * infinite or NaN; one out of it does not reach the row.  Results do not depend on the
- * order in which blocks run.  Starts that decrease or lie outside [0, T] or [0, S] are
- * taken into the range and counted in errors->bad_inputs (the rows of their
- * sequences are unspecified).
+ * fp32 rounding is a factor in the weight; a cap adds at most 2^-20 of the capped
+ * score); each weight is rounded to q's type before it meets its value (by up to 2^-8
+ * of itself in bf16, 2^-11 in fp16, small ones there by 2^-28 of the row's highest).
+ * Outputs of finite values (bf16: up to 2^127, fp16: 2^15) are finite at any length;
+ * bf16 ones are off by up to 2^-137 for every position seen besides.  An infinite or
+ * NaN value in a row's sight makes that output infinite or NaN; one out of it does not
+ * reach the row.  Results do not depend on the order in which blocks run.  Starts that
+ * decrease or lie outside [0, T] or [0, S] are taken into the range and counted in
+ * errors->bad_inputs (the rows of their sequences are unspecified).
  *   T <= 2^26, S <= 2^30, B <= 65535, Hq <= 4096.
  * ------------------------------------------------------------------------ */
 IDX_API idx_status idx_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,

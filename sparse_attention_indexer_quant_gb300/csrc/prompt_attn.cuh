@@ -70,14 +70,18 @@ using attn::ex2;
 using attn::kCapNear;
 using attn::kLn2;
 
-// log2 of the weight that a raise gives the highest score, and of how far the weights of
-// half a tile may pass it before the next raise (which costs 2900 cycles).  fp16 weights must
-// stay below 2^16, and under 2^-24 they are lost; bf16 ones have range to spare, which is
-// left to the values (sums are finite for values up to 2^110).
+// log2 of the weight that a raise gives the highest score, and of how far weights' sums
+// may pass it before the next raise (which costs 2900 cycles).
+// fp16: the sum of half a tile; weights must stay below 2^16, and under 2^-24 they are lost.
+// bf16: the sum of all weights so far, so that it never exceeds 1/2 and sums of values up to
+// 2^127 are finite at any length.  A raise leaves it 2^-15 or more, of which fp32's least step is
+// half of bf16's: small values keep what bf16 holds of them.  (Keys of equal scores raise it after
+// 16384 of them, then 16384 times as many.  Raises at 2^-1 over 2^-12 instead: 16384 tokens, 32/8
+// heads of 128, 1440 us for 1404, head_dim 256 with window and cap 185 for 180.)
 template <bool BF16>
-constexpr float kLift = BF16 ? 0.f : 3.f;
+constexpr float kLift = BF16 ? -15.f : 3.f;
 template <bool BF16>
-constexpr float kSlack = BF16 ? 16.f : 12.f;
+constexpr float kSlack = BF16 ? 14.f : 12.f;
 
 // mbar_wait (common.cuh) with the limit in cycles of the SM: reading the global timer
 // costs as much as a short wait, and every tile waits several times.
@@ -463,8 +467,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           float s[W];
           scores(s, h);
           uint32_t p[W / 2];
+          const float room = BF16 ? most - l : most;  // (known before the sum is)
           const float sum = weights(s, -m, p);
-          slow = __any_sync(~0u, sum > most);
+          slow = __any_sync(~0u, sum > room);
           if (!slow) {
             l += sum;
             store(at_p, p);
@@ -478,7 +483,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 #pragma unroll
           for (int c = 4; c < W; ++c) top[c & 3] = fmaxf(top[c & 3], s[c]);
           const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * mult;
-          const float up = live ? fmaxf(mx - kLift<BF16>, m) : m;
+          float up = live ? fmaxf(mx - kLift<BF16>, m) : m;
+          // (half a tile's new weights sum to 2^(lift + 7) at most; so may the earlier ones)
+          if (BF16 && live && l > exp2f(kLift<BF16> + 7.f)) up = fmaxf(up, m + __log2f(l) - kLift<BF16>);
           const float w = m == -INFINITY ? 0.f : ex2(m - up);
           if (i + h > 0) {
             if (!(h ? sums(i, 0) : sums(i - 1, C::kPieces - 1))) {
