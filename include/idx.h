@@ -517,9 +517,9 @@ IDX_API idx_status idx_rope_table(int64_t pos0, int64_t num_pos, int32_t rot_dim
  *              contiguous.
  * Arithmetic in fp32, rounded once into q_out or the cache; E4M3 codes hold
  * x / scale, rounded to nearest even, magnitudes past 448 saturate; MXFP4 codes follow
- * the rule above, by x as 64 bits give it (infinities and NaN are outside the contract there,
- * and so are values past 2^54 for the attention, which takes a key's block with scale
- * byte 0, of values below 2^-124, for zeros).
+ * the rule above, by x as 64 bits give it (infinities, NaN and x past fp32's range are
+ * outside the contract there, and so are values past 2^54 for the attention, which takes
+ * a key's block with scale byte 0, of values below 2^-124, for zeros).
  * A token whose position is outside the table is skipped whole, one whose slot
  * is outside [0, num_blocks*page_size) stores nothing; both are counted.
  * ------------------------------------------------------------------------ */

@@ -22,7 +22,7 @@
 // butterfly shuffles gives the scale byte, each lane stores four bytes of codes and the first
 // of the four the byte; warps of queries alone do not.  Keys are encoded twice, at both ends of
 // what their fp32 roundings leave open, and again in 64 bits where the two differ, so that codes
-// are those of the unrounded key (32768 tokens of 32 + 2 x 8 heads of 128, 707 MB: 162 us, 0.65 of
+// are those of the unrounded key (32768 tokens of 32 + 2 x 8 heads of 128, 707 MB: 168 us, 0.63 of
 // the copy rate; without this 142, where some 15 codes in 17 million fall to the other side of
 // their border; encoding in every warp 11 more; E4M3 143).
 #include "common.cuh"
@@ -131,6 +131,10 @@ __device__ __noinline__ void store_exactly(const KvInsertArgs& a, int q_groups, 
     }
 #pragma unroll
     for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
+    if (!__any_sync(~0u, ss != 0.)) {  // zeros, which need no arithmetic
+      if (store && u < gr.n) Place4(a, true, slot, gr.h0, part, D).store(u, 0, 0, part);
+      continue;
+    }
     if (a.k_weight != nullptr) {
       const double r = 1. / sqrt(ss / D + (double)a.eps);
 #pragma unroll
@@ -284,10 +288,14 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 9 : 8) kv_insert_kernel(
   // factor (half of 8 products' and sums', 5 shuffled sums' and eps's 14; 4 by rsqrtf; 2
   // products), 2 by the turn, 1 by the bounds below, in all 16 of the magnitudes that enter.
   // Where a code or a scale could differ within 17, for one or two vectors in a thousand, 64-bit
-  // arithmetic decides afterwards.
+  // arithmetic decides afterwards, and so it does where fp32 may be off by more: a mean square that
+  // overflows or, its eps letting it, is below 2^-100 (squares lose bits), a block whose largest is
+  // outside [2^-50, 2^60) and not zero (so may products lose bits, or overflow with a weight's).
+  // (32768 tokens 168 us, without these three 163.)
   const bool inexact = CACHE4 && kind == kKey && (weight != nullptr || turns);
   const bool checks = CACHE4 && __any_sync(~0u, inexact);
-  uint32_t unsure = 0;  // heads of the warp's groups
+  uint32_t unsure = 0;  // heads of the lane's group
+  const uint32_t least = a.eps >= 0x1p-100f ? 0 : 0x0D800000u;  // 2^-100
   float bound = inexact ? 0x1.1p-20f : 0.f;
   if (turns) {
     float top = 1.f;
@@ -298,6 +306,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 9 : 8) kv_insert_kernel(
 #pragma unroll
   for (int u = 0; u < VPT; ++u) {
     float x[8], off[4];
+    bool far = false;
     if (works || BITS < 16) unpack8<BF16>(raw[u], x);
     if (works) {
       float ss = 0.f;
@@ -306,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 9 : 8) kv_insert_kernel(
 #pragma unroll
       for (int d = 1; d < kLanes; d <<= 1) ss += __shfl_xor_sync(~0u, ss, d);
       if (weight != nullptr) {
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const float ms = ss * (1.f / D) + a.eps, r = rsqrtf(ms);
+        far = __float_as_uint(ms) - least >= 0x7F800000u - least;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
       }
@@ -349,7 +359,15 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 9 : 8) kv_insert_kernel(
         }
         uint32_t low;
         const bool same = encode8_block(y, &low) == (codes = encode8_block(x, &byte));
-        if (__any_sync(~0u, !same || low != byte)) unsure |= 1u << u;
+        bool lost = !same || low != byte || far;
+        if (byte - 77u >= 110u && inexact) {
+          // (x has moved away from zero: where it is zero still, nothing came near the least code)
+          float top = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+          lost = lost || top != 0.f;
+        }
+        if (lost) unsure |= 1u << u;
       } else {
         codes = encode8_block(x, &byte);
       }
@@ -376,7 +394,10 @@ __global__ void __launch_bounds__(kThreads, BITS == 8 ? 9 : 8) kv_insert_kernel(
       *reinterpret_cast<uint4*>(dst + u * dst_hs) = kind == kValue ? raw[u] : pack8<BF16>(x);
     }
   }
-  if (CACHE4 && unsure != 0) store_exactly<D, BF16, PAIRS, VPT>(a, q_groups, k_groups, unsure);
+  if (CACHE4 && checks) {
+    unsure = __reduce_or_sync(~0u, unsure);
+    if (unsure != 0) store_exactly<D, BF16, PAIRS, VPT>(a, q_groups, k_groups, unsure);
+  }
 }
 
 template <int D, bool BF16, int BITS, bool PAIRS>
