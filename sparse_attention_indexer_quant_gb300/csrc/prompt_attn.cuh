@@ -65,7 +65,6 @@
 namespace idx {
 namespace prompt {
 
-using attn::capped;
 using attn::ex2;
 using attn::kCapNear;
 using attn::kLn2;
@@ -405,14 +404,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         tmem_take(s);
         if (CAP) {
           // the near form by way of the products' own units, its factors times mult:
-          // s (f0 + z (f1 + z (f2 + ...))), z = (s / cap)^2
+          // s (f0 + z (f1 + z (f2 + ...))), z = (s / cap)^2.  Where some score of the warp's is past
+          // half a cap (one that a row does not see, perhaps another sequence's), those below go by
+          // the same operations all the same, so that no score's bits depend on its neighbours.
           float top = 0.f;
 #pragma unroll
           for (int c = 0; c < W; ++c) top = fmaxf(top, fabsf(s[c]));
-          const float k = a.mult * a.cap_inv;
+          const float k = a.cap_unit;
           if (__all_sync(~0u, top * k < kCapNear)) {
-            const float f0 = a.mult, f1 = attn::kCapNear1 * f0, f2 = attn::kCapNear2 * f0;
-            const float f3 = attn::kCapNear3 * f0, f4 = attn::kCapNear4 * f0;
+          const float f0 = a.mult, f1 = attn::kCapNear1 * f0, f2 = attn::kCapNear2 * f0;
+          const float f3 = attn::kCapNear3 * f0, f4 = attn::kCapNear4 * f0;
 #pragma unroll
             for (int c = 0; c < W; c += 2) {
               const float2 x = make_float2(s[c], s[c + 1]), y = mul2(x, make_float2(k, k)), z = mul2(y, y);
@@ -426,7 +427,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < W; ++c) s[c] = capped(s[c] * a.mult, a.cap_log2, a.cap_inv);
+            for (int c = 0; c < W; ++c) {
+              const float f0 = a.mult, f1 = attn::kCapNear1 * f0, f2 = attn::kCapNear2 * f0;
+              const float f3 = attn::kCapNear3 * f0, f4 = attn::kCapNear4 * f0;
+              const float y = s[c] * k, z = y * y;
+              const float near = fmaf(fmaf(fmaf(fmaf(f4, z, f3), z, f2), z, f1), z, f0) * s[c];
+              const float far = fmaf(__fdividef(-2.f, 1.f + ex2(2.f * attn::kLog2e * fabsf(y))), a.cap_log2, a.cap_log2);
+              s[c] = fabsf(y) < kCapNear ? near : copysignf(far, y);
+            }
           }
         }
         if (!whole) {
@@ -873,7 +881,7 @@ cudaError_t launch(const CUtensorMap* tm, const PromptArgs& a, cudaStream_t stre
 
 template <int D, bool BF16>
 cudaError_t launch_cap(const CUtensorMap* tm, const PromptArgs& a, cudaStream_t stream) {
-  return a.cap_inv > 0.f ? launch<D, BF16, true>(tm, a, stream) : launch<D, BF16, false>(tm, a, stream);
+  return a.cap_unit > 0.f ? launch<D, BF16, true>(tm, a, stream) : launch<D, BF16, false>(tm, a, stream);
 }
 
 template <bool BF16>

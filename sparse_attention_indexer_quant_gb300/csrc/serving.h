@@ -184,7 +184,7 @@ struct PromptArgs {
   int32_t split;     // CTAs of a cluster that share the same rows' keys: 1, 2, 4 or 8
   float mult;  // log2 score per product, positive
   int32_t neg;  // scores are the products' negatives
-  float cap_log2, cap_inv;  // as AttnArgs
+  float cap_log2, cap_unit;  // the cap in log2 units (0: no cap); caps per product
   int32_t window;  // 0: none
   int32_t causal;
   idx_device_errors* errors;

@@ -719,7 +719,7 @@ idx_status idx_prompt_attention(const void* q, int64_t q_token_stride, int64_t q
   if (softcap > 0.f) {
     const double cap = (double)softcap * 1.4426950408889634;
     a.cap_log2 = cap < FLT_MAX ? (float)cap : FLT_MAX;
-    a.cap_inv = (float)fmin(1.0 / cap, FLT_MAX);
+    a.cap_unit = (float)fmin(fmax(a.mult / cap, FLT_MIN), FLT_MAX);
   }
   a.window = window;
   a.causal = causal != 0;
