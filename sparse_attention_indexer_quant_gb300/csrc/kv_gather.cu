@@ -163,7 +163,7 @@ cudaError_t launch_dim(const KvGatherArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_kv_gather(const KvGatherArgs& a, int, cudaStream_t stream) {
+cudaError_t launch_kv_gather(const KvGatherArgs& a, cudaStream_t stream) {
   switch (a.kv.dtype) {
     case IDX_E4M3: return a.out_bf16 ? launch_dim<IDX_E4M3, true>(a, stream) : launch_dim<IDX_E4M3, false>(a, stream);
     case IDX_MXFP4: return a.out_bf16 ? launch_dim<IDX_MXFP4, true>(a, stream) : launch_dim<IDX_MXFP4, false>(a, stream);

@@ -68,8 +68,6 @@ struct KvInsertArgs {
   int32_t page_shift;
   idx_device_errors* errors;
 };
-// Bytes of a page of a 4-bit cache's head: its tokens' codes, then their scale bytes.
-constexpr int kv4_page_bytes(int head_dim, int page_size) { return page_size * (head_dim / 2 + head_dim / 32); }
 cudaError_t launch_kv_insert(int dtype, const KvInsertArgs& a, int sms, cudaStream_t stream);
 
 // Cached tokens into contiguous 16-bit rows.
@@ -86,7 +84,7 @@ struct KvGatherArgs {
   int32_t out_bf16;
   idx_device_errors* errors;
 };
-cudaError_t launch_kv_gather(const KvGatherArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_kv_gather(const KvGatherArgs& a, cudaStream_t stream);
 
 // Paged attention: resident CTAs over the device, and the levels of segments
 // they claim (see paged_attn.cuh), are bounded by these, so that the

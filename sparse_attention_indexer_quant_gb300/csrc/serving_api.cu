@@ -585,8 +585,7 @@ idx_status idx_gather_kv(const idx_kv_cache* kv, const int32_t* block_table, int
     return fail(IDX_ERR_INVALID_ARG, "max_blocks=%d", max_blocks);
   if (out_rows < 0 || out_rows > (int64_t)1 << 30)
     return fail(IDX_ERR_INVALID_ARG, "out_rows=%lld outside [0, 2^30]", (long long)out_rows);
-  int sms = 0;
-  s = idx::current_device_ok(&sms);
+  s = idx::current_device_ok(nullptr);
   if (s != IDX_OK) return s;
   if (B == 0 || out_rows == 0) return ok();
   if ((s = check_kv_pointers(kv)) != IDX_OK) return s;
@@ -608,7 +607,7 @@ idx_status idx_gather_kv(const idx_kv_cache* kv, const int32_t* block_table, int
   a.page_shift = page_shift_of(kv->page_size);
   a.out_bf16 = dtype == IDX_BF16;
   a.errors = errors;
-  return from_cuda(idx::launch_kv_gather(a, sms, (cudaStream_t)stream), "gather_kv launch");
+  return from_cuda(idx::launch_kv_gather(a, (cudaStream_t)stream), "gather_kv launch");
 }
 
 idx_status idx_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,
