@@ -513,6 +513,8 @@ IDX_API idx_status idx_rope_table(int64_t pos0, int64_t num_pos, int32_t rot_dim
  *              (i, i + rot_dim/2), then rot_dim is a multiple of 16.
  *              With rot_dim = 0 positions and tables are not read.
  *   slot_mapping [N] int64; -1 = no key and value to store (q is still written).
+ *              The others must be distinct: of two tokens of one slot parts of
+ *              both may stay (codes and scale bytes of a 4-bit block, too).
  *   q_out      [N, Hq, D], contiguous, of q's type; may be q itself where q is
  *              contiguous.
  * Arithmetic in fp32, rounded once into q_out or the cache; E4M3 codes hold
@@ -607,7 +609,7 @@ IDX_API idx_status idx_paged_attention(const void* q, int64_t q_token_stride, in
  * 16-bit values are copied; codes times their scale are rounded once (4-bit ones are exact
  * in bf16).  Starts that decrease or lie outside [0, out_rows] are taken into the range,
  * positions past max_blocks pages and those of pages outside the cache are not
- * written; all are counted in errors->bad_inputs.
+ * written; all are counted in errors->bad_inputs, for keys and for values.
  *   out_rows <= 2^30, B <= 65535.
  * ------------------------------------------------------------------------ */
 IDX_API idx_status idx_gather_kv(const idx_kv_cache* kv, const int32_t* block_table, int32_t max_blocks,
@@ -644,6 +646,10 @@ IDX_API idx_status idx_gather_kv(const idx_kv_cache* kv, const int32_t* block_ta
  * reach the row.  Results do not depend on the order in which blocks run.  Starts that
  * decrease or lie outside [0, T] or [0, S] are taken into the range and counted in
  * errors->bad_inputs (the rows of their sequences are unspecified).
+ * How rows and keys are shared out follows T, S, B and the heads, not the starts (which
+ * are on the device): few rows over many keys have their keys shared out where T and B
+ * are small and S / B is long.  A call whose T or B leaves room (a captured graph's), or
+ * one long sequence among many short ones, may take several times as long.
  *   T <= 2^26, S <= 2^30, B <= 65535, Hq <= 4096.
  * ------------------------------------------------------------------------ */
 IDX_API idx_status idx_prompt_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride,

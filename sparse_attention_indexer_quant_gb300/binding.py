@@ -552,7 +552,7 @@ def qk_norm_rope_insert(q, k, v, q_weight, k_weight, eps: float, positions, cos,
     """RMS norm of every query and key head (weights [D] fp32; None: no norm),
     rotary turn of their first rot_dim dimensions by table rows positions, and
     the insert of keys and values into the paged cache at slot_mapping (-1:
-    none), in one pass.  q [N, Hq, D], k and v [N, Hkv, D] bf16 or fp16, which
+    none, the others distinct), in one pass.  q [N, Hq, D], k and v [N, Hkv, D] bf16 or fp16, which
     may be slices of one projection; caches [num_blocks, Hkv, page_size, D] of
     the same type, float8_e4m3fn (codes hold x / scale) or 4-bit (new_kv_cache
     with "mxfp4"; infinities and NaN are outside its contract).  Returns the turned
@@ -636,7 +636,8 @@ def prompt_attention(q, k, v, query_start, key_start=None, scale: float | None =
     sequence's.  scale defaults to D^-0.5; softcap > 0 bounds scores by softcap *
     tanh(score / softcap).  Returns out [T, Hq, D] of q's type, with return_lse
     also ln sum exp of the scores ([T, Hq] fp32); rows outside all sequences are
-    not written."""
+    not written.  Few rows over many keys are fast where q, k and v have no more rows,
+    and the starts no more entries, than the sequences need."""
     o, l = _call(_serving.prompt_attention, stream, q, k, v, query_start, key_start, scale, softcap,
                  window, causal, out, lse, return_lse, errors)
     return (o, l) if return_lse else o
