@@ -50,10 +50,10 @@
 // (0.54 GB) 86 us, 6.3 TB/s, items whole by four warps each (split and joined
 // 94).  Rows gathered one by one take 0.92 of the copy rate at 256 bytes, 0.95 at
 // 512, 0.70 - 0.74 at 128.  The tensor pipe is 13 - 15 % busy with up to eight rows, 50 % with sixteen over an E4M3 cache; it binds
-// from 32 rows over an E4M3 cache on (0.53 of the copy rate).  Over 4-bit values the logic
-// pipe binds: 64 requests of 20480 keys 383 us, 0.55 of the copy rate, that pipe 59 % and the
-// issue slots 72 % busy (476 instructions for 16 keys of 128 dimensions, half of them to
-// turn codes into operands); selected positions by two places gathered a row, codes and scales.
+// from 32 rows over an E4M3 cache on (0.53 of the copy rate).  Over 4-bit values the
+// way from codes to operands binds: 64 requests of 20480 keys 383 us, 0.55 of the copy rate, the
+// issue slots 72 % and the logic pipe 59 % busy (476 instructions for 16 keys of 128 dimensions, half
+// of them on that way, in chains that 16 warps an SM do not hide); selected positions by two places gathered a row, codes and scales.
 #pragma once
 
 #include <float.h>

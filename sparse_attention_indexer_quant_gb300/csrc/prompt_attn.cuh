@@ -25,12 +25,12 @@
 // share the weight; a second term would add half of the tensor work again.  Sums of
 // weights are fp32 and taken before the rounding.
 //
-// Bound by the tensor core and the power: 16384 tokens, 32 heads on 8 of 128, causal, 1280 us,
-// 1.72 PFLOP/s (0.89 of the measured burst, 0.98 of the sustained rate); 8192 tokens
-// 342 us, 1.61, where the tensor pipe is busy 69 % of the time, starts and ends of CTAs
-// included (5 us each); head_dim 64 1.14 PFLOP/s, by the hand-overs between the roles, 1000
+// Bound by the tensor core and the power: 16384 tokens, 32 heads on 8 of 128, causal, 1390 us one
+// call after another, 1.58 PFLOP/s (0.82 of the measured burst, 0.90 of the sustained rate); 8192
+// tokens 343 us, 1.60, where the tensor pipe is busy 69 % of the time, starts and ends of CTAs
+// included (5 us each); head_dim 64 1.12 PFLOP/s, by the hand-overs between the roles, 1000
 // cycles a step (a lane for each row tile's products, or no exponentials at all: 0.83 of the
-// time at best); head_dim 256 1.46.
+// time at best); head_dim 256 1.54.
 //
 // A position that a row does not see has weight zero, but zero times an infinity is
 // NaN: in tiles where some row's sight begins or ends two warps look through the
@@ -39,7 +39,7 @@
 //
 // Few rows over many keys would leave most SMs idle: then the CTAs of a cluster take a
 // part each of the same rows' keys and join them through distributed shared memory, in the
-// order of the keys (16 new tokens behind 32768: 38 us, by one CTA each 224).
+// order of the keys (16 new tokens behind 32768: 37 us, by one CTA each 226).
 //
 // Roles (384 threads with two row tiles, 256 with one): warps 0-3 and 4-7 the softmax
 // of row tile 0 and 1; then a warp whose elected lane issues the products, one that
